@@ -93,7 +93,8 @@ NTX_API int ntx_version(void); /* major*10000 + minor*100 + patch */
  * copy did not land in time, 2 copies still outstanding when a CTA that gave
  * up had to exit (the context is then unusable: launch nothing more on it),
  * 3 a token id outside [0, V) reached the embedding, 4 a grid-wide barrier of
- * the persistent decode kernel ran out. */
+ * the persistent decode kernel ran out, 5 a sequence, position, length or
+ * page index outside a paged KV cache reached one of its kernels. */
 NTX_API int ntx_device_status(int* code);
 
 /* The bounds-checked debug build (compiled with NTX_CHECK; no counterpart in
@@ -233,6 +234,125 @@ NTX_API int ntx_attn_decode_static(const float* q, const uint16_t* k_cache, cons
 /* SwiGLU out_i = silu(gate_i) up_i, silu(z) = z / (1 + e^-z) ([README]
  * 主な機能: SwiGLU).  Device fp32[n] each; out may alias either input. */
 NTX_API int ntx_swiglu(const float* gate, const float* up, float* out, int64_t n, void* stream);
+
+/* ------------------------------------------------------------ paged KV cache
+ * A key-value cache for many sequences in one pool of memory, in fp16 or in
+ * the block types of the weights, with the calls a decode step of such a model
+ * makes: head norms with the rotation, the cache's write, the attention of one
+ * new token per sequence, and the cache read back ([README] 主な機能: GQA, KV
+ * cache, RoPE, RMSNorm; the pages describe one sequence with a contiguous fp16
+ * cache, so pages, block types and head norms are this library's).
+ *
+ * Pool: k_pages and v_pages each hold n_pages pages of ntx_paged_kv_bytes /
+ * n_pages bytes.  A page holds page_size positions of every KV head; the part
+ * of one head is contiguous: first the codes of its page_size rows, then (block
+ * types) its scales, one fp16 for each row and 32 elements:
+ *   NTX_F16:  [page_size][head_dim] fp16, no scales;
+ *   NTX_Q8_0: [page_size][head_dim] int8 q, scales d;            value = d q
+ *   NTX_Q4_0: [page_size][head_dim/2], byte j of a 32-element block holds
+ *             element j in its low and j + 16 in its high nibble;  value = d (q - 8)
+ * i.e. the numbers of the GGUF blocks, with codes and scales apart so that both
+ * are aligned.  With one page of max_ctx rows per sequence an NTX_F16 pool is
+ * the contiguous cache of ntx_attn_decode.
+ * page_table: device int32 [n_seqs][max_pages]; entry j of a row is the page of
+ * positions j*page_size .. (j+1)*page_size - 1 of that sequence.  Sequences may
+ * share pages that none of them writes; entries past a sequence's length are
+ * not read and may hold anything.
+ * Limits: head_dim 64, 128 or 256; page_size a multiple of 16; max_pages *
+ * page_size <= 2^30; n_kv_heads <= 1024; n_seqs <= 1024; pools 16-byte aligned.
+ * Kernels check every sequence, position, length and page index they read from
+ * device memory; what lies outside the cache is never accessed, and sets
+ * device status 5 (each call says what it does instead). */
+typedef struct {
+  int32_t type;       /* NTX_F16, NTX_Q8_0 or NTX_Q4_0, both pools */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;  /* positions per page */
+  int32_t n_pages;    /* pages in each pool */
+  int32_t n_seqs;     /* rows of page_table */
+  int32_t max_pages;  /* entries per row of page_table */
+  void* k_pages;
+  void* v_pages;
+  const int32_t* page_table;
+} ntx_paged_kv;
+
+/* Bytes of one pool (k_pages or v_pages); 0 on bad arguments. */
+NTX_API uint64_t ntx_paged_kv_bytes(int type, int n_kv_heads, int head_dim, int page_size, int n_pages);
+
+/* RMSNorm of every query and key head and the rotation, in one pass.  For each
+ * token n and head, x the head's head_dim values:
+ *   y = w x / sqrt(mean_j x_j^2 + eps)           (w = wq or wk; NULL: ones)
+ *   out pair i = (a cos - b sin, a sin + b cos), angle positions[n] *
+ *   theta^(-2i/rot_dim), i < rot_dim/2, with (a, b) = elements (2i, 2i+1)
+ *   (NTX_ROPE_ADJACENT, the pairing of ntx_rope) or (i, i + rot_dim/2)
+ *   (NTX_ROPE_HALVES); elements from rot_dim on are only normed.
+ * Angles are formed in fp64, the rest in fp32.
+ *   q, q_out: device fp32, token n's n_q_heads x head_dim values start at
+ *   n * q_stride floats; k, k_out: n_kv_heads x head_dim at n * k_stride.
+ *   q_out may be q and k_out may be k; any other overlap of an output with an
+ *   input's rows is not allowed.  wq, wk: device fp32[head_dim].
+ *   positions: device int32[n_tokens]; a negative one marks an unused row,
+ *   whose outputs are left as they were.
+ * head_dim even, 2..256; rot_dim even, 0..head_dim; strides at least the row
+ * (q_stride >= n_q_heads * head_dim); q (k) may be NULL when n_q_heads
+ * (n_kv_heads) is 0; n_tokens 0 does nothing. */
+#define NTX_ROPE_ADJACENT 0
+#define NTX_ROPE_HALVES 1
+NTX_API int ntx_qk_norm_rope(const float* q, const float* k, float* q_out, float* k_out, int64_t q_stride,
+                             int64_t k_stride, const float* wq, const float* wk, const int32_t* positions,
+                             int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int rot_dim, int pairing,
+                             float theta, float eps, void* stream);
+
+/* Writes n_tokens rows of keys and values to the cache, quantised to its type.
+ *   k, v: device fp32, token n's n_kv_heads x head_dim values at n * k_stride
+ *   (v_stride) floats; 4-byte aligned (16-byte aligned rows are faster).
+ *   seq_ids: device int32[n_tokens], the sequence of each token; NULL: token n
+ *   belongs to sequence n (then n_tokens <= n_seqs).
+ *   positions: device int32[n_tokens]; a negative one marks an unused row,
+ *   which is not written.
+ * Each block of 32 is the block the weights' formats hold for the same fp32
+ * values: NTX_Q8_0 d = max|w| / 127, q = w / d; NTX_Q4_0 d = (first element of
+ * the largest |w|) / -8, q = w / d + 8 in 0..15; quotients in fp32, codes
+ * rounded half away from zero, d then rounded to fp16.  So a block's values
+ * must stay below 127 (8) * 65504 in magnitude; beyond, d is infinite.  A block
+ * that holds a NaN or an infinity gets the scale NaN and reads back as NaN.
+ * NTX_F16 rounds to nearest even.
+ * A token whose sequence, position or page is outside the cache is skipped
+ * (status 5).  The (sequence, position) pairs of a call, and the pages they
+ * lie in, must be distinct places: two tokens for one place leave either's
+ * data, or a mixture, in it.  n_tokens 0 does nothing. */
+NTX_API int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_t k_stride, int64_t v_stride,
+                          const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* stream);
+
+/* Reads rows back as fp32: row n of k (v) receives the key (value) that the
+ * cache holds at (seq_ids[n], positions[n]).  Arguments as in ntx_kv_append;
+ * k or v may be NULL.  Values are exact (d q fits fp32).  Rows with a negative
+ * position, and rows whose place is outside the cache (status 5), are left as
+ * they were. */
+NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, int64_t v_stride,
+                        const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* stream);
+
+/* Attention of one new token per sequence over the paged cache: for sequence s
+ * and query head h (KV head h / (n_q_heads/n_kv_heads)),
+ *   out[s][h] = sum_{p < ctx_lens[s]} softmax_p(scale q[s][h].k_p) v_p,
+ * zeros where ctx_lens[s] is 0.  Scores, softmax statistics and sums are fp32.
+ *   q: device fp32, sequence s's n_q_heads x head_dim values at s * q_stride
+ *   floats.  out: device fp32 [n_seqs][n_q_heads][head_dim], not overlapping q.
+ *   ctx_lens: device int32[n_seqs]; counts the new token, whose key and value
+ *   the caller has already appended.  The lengths may change between replays
+ *   of a captured graph.
+ *   workspace: device, >= ntx_attn_paged_workspace_bytes(kv, n_q_heads), 16-byte
+ *   aligned; scratch only, contents on entry ignored.  Calls that may overlap
+ *   on the GPU need workspaces of their own.
+ * Limits: n_kv_heads | n_q_heads, at most 64 query heads per KV head; scale
+ * finite; q and out 16-byte aligned, q_stride a multiple of 4.
+ * A length below 0 counts as 0 and one past max_pages * page_size as that; a
+ * page outside the pool reads as keys and values of zero (status 5 for each).
+ * Cache rows past a sequence's length are not used, whatever they hold. */
+NTX_API size_t ntx_attn_paged_workspace_bytes(const ntx_paged_kv* kv, int n_q_heads);
+NTX_API int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_q_heads,
+                                  const int32_t* ctx_lens, float scale, void* workspace, size_t ws_bytes,
+                                  void* stream);
 
 /* ------------------------------------------------------------ layer / model */
 typedef struct {

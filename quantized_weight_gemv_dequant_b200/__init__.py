@@ -29,6 +29,7 @@ NTX_ERR_NOMEM = -7
 NTX_F32, NTX_F16, NTX_Q4_0, NTX_Q8_0, NTX_Q4_K, NTX_Q5_K, NTX_Q6_K = 0, 1, 2, 8, 12, 13, 14
 NTX_MIXED = -1
 NTX_CALIBRATE_SKIP, NTX_USE_SKIP, NTX_NO_GRAPH, NTX_NO_PERSIST = 1, 2, 4, 8
+NTX_ROPE_ADJACENT, NTX_ROPE_HALVES = 0, 1
 
 BLOCK_ELEMS = {NTX_F32: 1, NTX_F16: 1, NTX_Q4_0: 32, NTX_Q8_0: 32, NTX_Q4_K: 256, NTX_Q5_K: 256, NTX_Q6_K: 256}
 BLOCK_BYTES = {NTX_F32: 4, NTX_F16: 2, NTX_Q4_0: 18, NTX_Q8_0: 34, NTX_Q4_K: 144, NTX_Q5_K: 176, NTX_Q6_K: 210}
@@ -43,6 +44,8 @@ EXPORTS = (
     "ntx_persistent_plan", "ntx_layer_layout_mixed", "ntx_engine_device_bytes", "ntx_auto_tier_map",
     "ntx_memory_budget", "ntx_set_host_wait_limit", "ntx_engine_set_fault", "ntx_decode_spec",
     "ntx_set_persist_two_types", "ntx_check_enabled", "ntx_check_report", "ntx_hbm_read_probe",
+    "ntx_paged_kv_bytes", "ntx_qk_norm_rope", "ntx_kv_append", "ntx_kv_read", "ntx_attn_paged_workspace_bytes",
+    "ntx_attn_decode_paged",
 )
 
 
@@ -63,6 +66,12 @@ class ntx_layer_weights(ctypes.Structure):
     _fields_ = [("qtype", ctypes.c_int32), ("base", ctypes.c_void_p)] + [
         (n, ctypes.c_uint64) for n in ("off_wq", "off_wk", "off_wv", "off_wo", "off_wg", "off_wu", "off_wd",
                                        "off_attn_norm", "off_ffn_norm")] + [("mat_qtype", ctypes.c_int32 * 7)]
+
+
+class ntx_paged_kv(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("type", "n_kv_heads", "head_dim", "page_size", "n_pages", "n_seqs",
+                                              "max_pages")] + [
+        (n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table")]
 
 
 _lib = None
@@ -95,6 +104,13 @@ def lib():
             "ntx_attn_workspace_bytes": ([i32, i32, i32, i32], sz),
             "ntx_attn_decode": ([vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, sz, vp], i32),
             "ntx_swiglu": ([vp, vp, vp, i64, vp], i32),
+            "ntx_paged_kv_bytes": ([i32, i32, i32, i32, i32], ctypes.c_uint64),
+            "ntx_qk_norm_rope": ([vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp],
+                                 i32),
+            "ntx_kv_append": ([P(ntx_paged_kv), vp, vp, i64, i64, vp, vp, i32, vp], i32),
+            "ntx_kv_read": ([P(ntx_paged_kv), vp, vp, i64, i64, vp, vp, i32, vp], i32),
+            "ntx_attn_paged_workspace_bytes": ([P(ntx_paged_kv), i32], sz),
+            "ntx_attn_decode_paged": ([P(ntx_paged_kv), vp, i64, vp, i32, vp, f32, vp, sz, vp], i32),
             "ntx_layer_layout": ([P(ntx_model_config), i32, P(ntx_layer_weights)], ctypes.c_uint64),
             "ntx_layer_layout_mixed": ([P(ntx_model_config), P(ctypes.c_int32), P(ntx_layer_weights)],
                                        ctypes.c_uint64),
@@ -232,6 +248,49 @@ def ntx_attn_decode_static(q, k_cache, v_cache, out, n_q_heads, n_kv_heads, head
 
 def ntx_swiglu(gate, up, out, n, stream=None):
     _check(lib().ntx_swiglu(_p(gate), _p(up), _p(out), n, _s(stream)))
+
+
+# ---------------------------------------------------------------- paged KV cache
+def make_paged_kv(type, n_kv_heads, head_dim, page_size, n_pages, k_pages, v_pages, page_table, n_seqs,
+                  max_pages) -> ntx_paged_kv:
+    """The cache a paged call works on: pools of ntx_paged_kv_bytes(...) bytes each and a device int32
+    [n_seqs][max_pages] table.  The caller keeps the three buffers alive while calls use them."""
+    return ntx_paged_kv(type, n_kv_heads, head_dim, page_size, n_pages, n_seqs, max_pages, _p(k_pages), _p(v_pages),
+                        _p(page_table))
+
+
+def ntx_paged_kv_bytes(type, n_kv_heads, head_dim, page_size, n_pages) -> int:
+    n = lib().ntx_paged_kv_bytes(type, n_kv_heads, head_dim, page_size, n_pages)
+    if n == 0:
+        raise NtxError(NTX_ERR_INVALID_ARG, "ntx_paged_kv_bytes: bad type or sizes")
+    return int(n)
+
+
+def ntx_qk_norm_rope(q, k, q_out, k_out, q_stride, k_stride, wq, wk, positions, n_tokens, n_q_heads, n_kv_heads,
+                     head_dim, rot_dim, pairing, theta, eps, stream=None):
+    _check(lib().ntx_qk_norm_rope(_p(q), _p(k), _p(q_out), _p(k_out), q_stride, k_stride, _p(wq), _p(wk),
+                                  _p(positions), n_tokens, n_q_heads, n_kv_heads, head_dim, rot_dim, pairing, theta,
+                                  eps, _s(stream)))
+
+
+def ntx_kv_append(kv: ntx_paged_kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, stream=None):
+    _check(lib().ntx_kv_append(kv, _p(k), _p(v), k_stride, v_stride, _p(seq_ids), _p(positions), n_tokens,
+                               _s(stream)))
+
+
+def ntx_kv_read(kv: ntx_paged_kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, stream=None):
+    _check(lib().ntx_kv_read(kv, _p(k), _p(v), k_stride, v_stride, _p(seq_ids), _p(positions), n_tokens,
+                             _s(stream)))
+
+
+def ntx_attn_paged_workspace_bytes(kv: ntx_paged_kv, n_q_heads) -> int:
+    return lib().ntx_attn_paged_workspace_bytes(kv, n_q_heads)
+
+
+def ntx_attn_decode_paged(kv: ntx_paged_kv, q, q_stride, out, n_q_heads, ctx_lens, scale, workspace, ws_bytes,
+                          stream=None):
+    _check(lib().ntx_attn_decode_paged(kv, _p(q), q_stride, _p(out), n_q_heads, _p(ctx_lens), scale, _p(workspace),
+                                       ws_bytes, _s(stream)))
 
 
 # ---------------------------------------------------------------- layer / model

@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(HERE, "libntx.so")
 CHECK_SO = os.path.join(HERE, "libntx_check.so")  # the bounds-checked debug build (NTX_CHECK)
-SOURCES = ["kernels.cu", "api.cu", "noalloc.cu", "persist.cu", "tiers.cu"]
+SOURCES = ["kernels.cu", "api.cu", "noalloc.cu", "paged.cu", "persist.cu", "tiers.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -24,6 +24,7 @@ enum : int {
   kStatusDrainTimeout = 2,
   kStatusBadToken = 3,
   kStatusGridTimeout = 4,  // a grid-wide barrier of the persistent decode kernel ran out
+  kStatusBadPage = 5,      // a sequence, position, length or page index outside a paged KV cache
 };
 
 // Bounds checks of a debug build (compiled with NTX_CHECK): chk() is true

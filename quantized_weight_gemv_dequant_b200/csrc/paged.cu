@@ -1,0 +1,225 @@
+// paged.cu -- the C entries of the paged KV cache: argument checks and launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "launch.h"
+#include "ntx.h"
+#include "paged.cuh"
+
+namespace ntx {
+namespace {
+
+constexpr int kMaxPagedSeqs = 1024;
+constexpr int kMaxGroup = 64;
+
+int failf(int code, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return record_error(code, buf);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Bytes from the first to the last float of n rows.
+uint64_t span(int64_t n, int64_t stride, int64_t width) { return n < 1 ? 0 : ((n - 1) * stride + width) * 4ull; }
+
+int row_bytes(int type, int D) {
+  switch (type) {
+    case NTX_F16: return kv_row_bytes<kKvF16>(D);
+    case NTX_Q8_0: return kv_row_bytes<kKvQ8>(D);
+    case NTX_Q4_0: return kv_row_bytes<kKvQ4>(D);
+    default: return 0;
+  }
+}
+
+int check_sizes(const char* who, int type, int n_kv_heads, int head_dim, int page_size, int n_pages) {
+  if (!row_bytes(type, 128)) return failf(NTX_ERR_QTYPE, "%s: cache type %d is none of F16, Q8_0, Q4_0", who, type);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return failf(NTX_ERR_SHAPE, "%s: head_dim %d is none of 64, 128, 256", who, head_dim);
+  if (n_kv_heads < 1 || n_kv_heads > 1024) return failf(NTX_ERR_SHAPE, "%s: n_kv_heads %d outside 1..1024", who, n_kv_heads);
+  if (page_size < 16 || page_size % 16 || page_size > (1 << 30))
+    return failf(NTX_ERR_SHAPE, "%s: page_size %d is not a multiple of 16 up to 2^30", who, page_size);
+  if (n_pages < 1) return failf(NTX_ERR_SHAPE, "%s: n_pages %d", who, n_pages);
+  return NTX_OK;
+}
+
+int check_kv(const char* who, const ntx_paged_kv* kv) {
+  if (!kv) return failf(NTX_ERR_INVALID_ARG, "%s: kv is NULL", who);
+  const int rc = check_sizes(who, kv->type, kv->n_kv_heads, kv->head_dim, kv->page_size, kv->n_pages);
+  if (rc) return rc;
+  if (kv->n_seqs < 1 || kv->n_seqs > kMaxPagedSeqs)
+    return failf(NTX_ERR_SHAPE, "%s: n_seqs %d outside 1..%d", who, kv->n_seqs, kMaxPagedSeqs);
+  if (kv->max_pages < 1 || (int64_t)kv->max_pages * kv->page_size > (1 << 30))
+    return failf(NTX_ERR_SHAPE, "%s: max_pages %d x page_size %d outside 1..2^30", who, kv->max_pages, kv->page_size);
+  return NTX_OK;
+}
+
+int check_kv_pointers(const char* who, const ntx_paged_kv* kv) {
+  if (!kv->k_pages || !kv->v_pages || !kv->page_table) return failf(NTX_ERR_INVALID_ARG, "%s: NULL cache pointer", who);
+  if (!aligned(kv->k_pages, 16) || !aligned(kv->v_pages, 16) || !aligned(kv->page_table, 4))
+    return failf(NTX_ERR_ALIGN, "%s: pools must be 16-byte and page_table 4-byte aligned", who);
+  return NTX_OK;
+}
+
+// What ntx_kv_append and ntx_kv_read share.
+int check_tokens(const char* who, const ntx_paged_kv* kv, const float* k, const float* v, int64_t ks, int64_t vs,
+                 const int32_t* seq_ids, const int32_t* positions, int n_tokens) {
+  int rc = check_kv(who, kv);
+  if (rc) return rc;
+  const int64_t width = (int64_t)kv->n_kv_heads * kv->head_dim;
+  if (n_tokens < 0) return failf(NTX_ERR_SHAPE, "%s: n_tokens %d", who, n_tokens);
+  if (!seq_ids && n_tokens > kv->n_seqs)
+    return failf(NTX_ERR_SHAPE, "%s: %d tokens without seq_ids for %d sequences", who, n_tokens, kv->n_seqs);
+  if ((k && ks < width) || (v && vs < width))
+    return failf(NTX_ERR_SHAPE, "%s: row stride below n_kv_heads * head_dim = %lld", who, (long long)width);
+  if (n_tokens == 0) return NTX_OK;
+  if (!positions) return failf(NTX_ERR_INVALID_ARG, "%s: positions is NULL", who);
+  if (!aligned(k, 4) || !aligned(v, 4) || !aligned(seq_ids, 4) || !aligned(positions, 4))
+    return failf(NTX_ERR_ALIGN, "%s: pointers must be 4-byte aligned", who);
+  return check_kv_pointers(who, kv);
+}
+
+bool rows16(const float* p, int64_t stride) { return aligned(p, 16) && stride % 4 == 0; }
+
+template <class F>
+cudaError_t with_type(int type, F f) {
+  switch (type) {
+    case NTX_F16: return f(std::integral_constant<int, kKvF16>{});
+    case NTX_Q8_0: return f(std::integral_constant<int, kKvQ8>{});
+    default: return f(std::integral_constant<int, kKvQ4>{});
+  }
+}
+
+template <class F>
+cudaError_t with_dim(int D, F f) {
+  switch (D) {
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    default: return f(std::integral_constant<int, 256>{});
+  }
+}
+
+int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }
+
+}  // namespace
+}  // namespace ntx
+
+using namespace ntx;
+
+extern "C" {
+
+uint64_t ntx_paged_kv_bytes(int type, int n_kv_heads, int head_dim, int page_size, int n_pages) {
+  if (check_sizes("ntx_paged_kv_bytes", type, n_kv_heads, head_dim, page_size, n_pages)) return 0;
+  const unsigned __int128 n = (unsigned __int128)row_bytes(type, head_dim) * page_size * n_kv_heads * n_pages;
+  if (n >> 62) {
+    failf(NTX_ERR_SHAPE, "ntx_paged_kv_bytes: the pool is larger than 2^62 bytes");
+    return 0;
+  }
+  return (uint64_t)n;
+}
+
+int ntx_qk_norm_rope(const float* q, const float* k, float* q_out, float* k_out, int64_t q_stride, int64_t k_stride,
+                     const float* wq, const float* wk, const int32_t* positions, int n_tokens, int n_q_heads,
+                     int n_kv_heads, int head_dim, int rot_dim, int pairing, float theta, float eps, void* stream) {
+  const char* who = "ntx_qk_norm_rope";
+  if (head_dim < 2 || head_dim > 256 || head_dim % 2) return failf(NTX_ERR_SHAPE, "%s: head_dim %d", who, head_dim);
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2) return failf(NTX_ERR_SHAPE, "%s: rot_dim %d", who, rot_dim);
+  if (n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0 || n_q_heads > 65536 || n_kv_heads > 65536)
+    return failf(NTX_ERR_SHAPE, "%s: %d tokens, %d and %d heads", who, n_tokens, n_q_heads, n_kv_heads);
+  if (pairing != NTX_ROPE_ADJACENT && pairing != NTX_ROPE_HALVES)
+    return failf(NTX_ERR_INVALID_ARG, "%s: pairing %d", who, pairing);
+  if (!(theta > 0.f) || !std::isfinite(theta) || !(eps >= 0.f) || !std::isfinite(eps))
+    return failf(NTX_ERR_INVALID_ARG, "%s: bad theta or eps", who);
+  const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
+  if (q_stride < nq || k_stride < nk) return failf(NTX_ERR_SHAPE, "%s: stride below the row", who);
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return NTX_OK;
+  if (!positions || (nq && (!q || !q_out)) || (nk && (!k || !k_out)))
+    return failf(NTX_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(q, 4) || !aligned(k, 4) || !aligned(q_out, 4) || !aligned(k_out, 4) || !aligned(wq, 4) ||
+      !aligned(wk, 4) || !aligned(positions, 4))
+    return failf(NTX_ERR_ALIGN, "%s: pointers must be 4-byte aligned", who);
+  const uint64_t bq = span(n_tokens, q_stride, nq), bk = span(n_tokens, k_stride, nk);
+  if ((nq && q != q_out && overlap(q, bq, q_out, bq)) || (nk && k != k_out && overlap(k, bk, k_out, bk)))
+    return failf(NTX_ERR_INVALID_ARG, "%s: an output partially overlaps its input", who);
+  const int64_t rows = (int64_t)n_tokens * (n_q_heads + n_kv_heads);
+  const int grid = (int)min64((rows + 7) / 8, (int64_t)sm_count() * 8);
+  qk_norm_rope_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(q, k, q_out, k_out, q_stride, k_stride, wq, wk,
+                                                             positions, n_tokens, n_q_heads, n_kv_heads, head_dim,
+                                                             rot_dim, pairing, theta, eps);
+  return finish(who, cudaGetLastError());
+}
+
+int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_t k_stride, int64_t v_stride,
+                  const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* stream) {
+  const char* who = "ntx_kv_append";
+  const int rc = check_tokens(who, kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens);
+  if (rc || n_tokens == 0) return rc;
+  if (!k || !v) return failf(NTX_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  const bool vec = rows16(k, k_stride) && rows16(v, v_stride);
+  const dim3 grid((unsigned)min64(n_tokens, (int64_t)sm_count() * 64), 2);
+  return finish(who, with_type(kv->type, [&](auto t) {
+    kv_append_kernel<decltype(t)::value><<<grid, 256, 0, (cudaStream_t)stream>>>(
+        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, device_status_ptr());
+    return cudaGetLastError();
+  }));
+}
+
+int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, int64_t v_stride,
+                const int32_t* seq_ids, const int32_t* positions, int n_tokens, void* stream) {
+  const char* who = "ntx_kv_read";
+  const int rc = check_tokens(who, kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens);
+  if (rc || n_tokens == 0 || (!k && !v)) return rc;
+  const dim3 grid((unsigned)min64(n_tokens, (int64_t)sm_count() * 64), 2);
+  return finish(who, with_type(kv->type, [&](auto t) {
+    kv_read_kernel<decltype(t)::value><<<grid, 256, 0, (cudaStream_t)stream>>>(
+        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, device_status_ptr());
+    return cudaGetLastError();
+  }));
+}
+
+size_t ntx_attn_paged_workspace_bytes(const ntx_paged_kv* kv, int n_q_heads) {
+  const char* who = "ntx_attn_paged_workspace_bytes";
+  if (check_kv(who, kv) || n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > kMaxGroup) return 0;
+  return 256;
+}
+
+int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_q_heads,
+                          const int32_t* ctx_lens, float scale, void* workspace, size_t ws_bytes, void* stream) {
+  const char* who = "ntx_attn_decode_paged";
+  int rc = check_kv(who, kv);
+  if (rc) return rc;
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > kMaxGroup)
+    return failf(NTX_ERR_SHAPE, "%s: %d query heads over %d KV heads", who, n_q_heads, kv->n_kv_heads);
+  const int64_t width = (int64_t)n_q_heads * kv->head_dim;
+  if (q_stride < width) return failf(NTX_ERR_SHAPE, "%s: q_stride below n_q_heads * head_dim", who);
+  if (!std::isfinite(scale)) return failf(NTX_ERR_INVALID_ARG, "%s: scale is not finite", who);
+  if (!q || !out || !ctx_lens || !workspace) return failf(NTX_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if ((rc = check_kv_pointers(who, kv)) != NTX_OK) return rc;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_stride % 4 || !aligned(workspace, 16) || !aligned(ctx_lens, 4))
+    return failf(NTX_ERR_ALIGN, "%s: q, its rows, out and workspace must be 16-byte aligned", who);
+  if (overlap(q, span(kv->n_seqs, q_stride, width), out, span(kv->n_seqs, width, width)))
+    return failf(NTX_ERR_INVALID_ARG, "%s: out overlaps q", who);
+  if (ws_bytes < ntx_attn_paged_workspace_bytes(kv, n_q_heads))
+    return failf(NTX_ERR_NOMEM, "%s: workspace too small", who);
+  const dim3 grid(n_q_heads, kv->n_seqs);
+  return finish(who, with_type(kv->type, [&](auto t) {
+    return with_dim(kv->head_dim, [&](auto d) {
+      attn_paged_kernel<decltype(t)::value, decltype(d)::value><<<grid, 128, 0, (cudaStream_t)stream>>>(
+          *kv, q, q_stride, out, n_q_heads, ctx_lens, scale, device_status_ptr());
+      return cudaGetLastError();
+    });
+  }));
+}
+
+}  // extern "C"
