@@ -1,6 +1,7 @@
 // paged.cu -- the C entries of the paged KV cache: argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -110,6 +111,61 @@ cudaError_t with_dim(int D, F f) {
   }
 }
 
+// Kernel attributes are set on first use on a device.
+template <class K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  return e;
+}
+
+// Workspace: a record for each warp of the attention kernel, then two parts for each.
+size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
+  size_t n = 0;
+  with_type(kv->type, [&](auto t) {
+    return with_dim(kv->head_dim, [&](auto d) {
+      using F = PagedCfg<decltype(t)::value, decltype(d)::value>;
+      const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
+      const int G = n_q_heads / kv->n_kv_heads;
+      n = warps * (sizeof(int4) + 2 * sizeof(float) * paged_part_floats(G < 8 ? G : 8, kv->head_dim));
+      return cudaSuccess;
+    });
+  });
+  return n;
+}
+
+template <int T, int D>
+cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
+                              const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
+  using F = PagedCfg<T, D>;
+  static std::atomic<unsigned long long> done{0}, done_join{0};
+  const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS;
+  int4* splits = static_cast<int4*>(ws);
+  float* part = reinterpret_cast<float*>(splits + warps);
+  cudaError_t e = allow_smem(attn_paged_kernel<T, D>, F::SMEM, done);
+  if (e == cudaSuccess) e = allow_smem(attn_paged_join_kernel<D>, 64 * 1024, done_join);
+  if (e != cudaSuccess) return e;
+  attn_paged_kernel<T, D><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, splits, part, Hq, lens, scale,
+                                                                   device_status_ptr());
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sm_count() * 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = warps * sizeof(int4);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int4*)splits, warps, (const float*)part, out, Hq,
+                            (int)kv.n_kv_heads);
+}
+
 int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }
 
 }  // namespace
@@ -191,7 +247,7 @@ int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, in
 size_t ntx_attn_paged_workspace_bytes(const ntx_paged_kv* kv, int n_q_heads) {
   const char* who = "ntx_attn_paged_workspace_bytes";
   if (check_kv(who, kv) || n_q_heads < 1 || n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > kMaxGroup) return 0;
-  return 256;
+  return paged_ws(kv, n_q_heads);
 }
 
 int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_q_heads,
@@ -212,12 +268,10 @@ int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stri
     return failf(NTX_ERR_INVALID_ARG, "%s: out overlaps q", who);
   if (ws_bytes < ntx_attn_paged_workspace_bytes(kv, n_q_heads))
     return failf(NTX_ERR_NOMEM, "%s: workspace too small", who);
-  const dim3 grid(n_q_heads, kv->n_seqs);
   return finish(who, with_type(kv->type, [&](auto t) {
     return with_dim(kv->head_dim, [&](auto d) {
-      attn_paged_kernel<decltype(t)::value, decltype(d)::value><<<grid, 128, 0, (cudaStream_t)stream>>>(
-          *kv, q, q_stride, out, n_q_heads, ctx_lens, scale, device_status_ptr());
-      return cudaGetLastError();
+      return launch_attn_paged<decltype(t)::value, decltype(d)::value>(*kv, q, q_stride, out, n_q_heads, ctx_lens,
+                                                                       scale, workspace, (cudaStream_t)stream);
     });
   }));
 }

@@ -7,12 +7,20 @@ squares is off by at most log2-depth-plus-lane-steps 2^-24 (<= 16 of them, half
 of that through the root), division, root, two products, then cos and sin
 rounded to fp32 and three operations, at most 20 half-steps of 2^-24 in all
 (1.2e-6).  Attention: with e = 2^-23,
-  |diff| <= (2 ds + (n/16 + 64) e) sum_p p_p |v_p|,
+  |diff| <= (2 ds + (n/16 + 64) e) sum_p p_p |v_p| + n 2^-38 max|v|,
   ds = (D + 8) e max_p (scale sum_i |q_i k_i|) + 4 e max_p |s_p|
 (ds: a score's error with every one of its D products and sums off by a step,
 and the scaling and the exponential's argument; a probability moves by at most
 2 ds relative, numerator and sum together; the weighted sums take at most one
-rounding for every 16 positions and 64 for the joins)."""
+rounding for every 16 positions and 64 for the joins).  The last term: p times
+the values' scale enters the products as a sum of two fp16 numbers after a power
+of two that puts the chunk's largest possible product in [2^13, 2^14].  The
+second number is rounded to the nearest multiple of 2^-24 where it is subnormal,
+an error of at most 2^-25 whatever p, i.e. 2^-25 / 2^13 = 2^-38 of the largest
+scale, times the code: at most 2^-38 max|v| for each of the n positions, however
+small its p.  (Where one position takes all and its value is zero, that is all
+there is: without the term, 4-bit values of exactly zero would demand an output
+right to 2^-15 of a weight of 1e-10.)"""
 import numpy as np
 import pytest
 
@@ -140,7 +148,8 @@ def attention_ref(cache, q, lens, hq, scale):
             p /= p.sum()
             out[s, h] = p @ v[h // g]
             ds = (cache.d + 8) * STEP * abs(scale) * (np.abs(k[h // g]) @ np.abs(a)).max() + 4 * STEP * np.abs(x).max()
-            bound[s, h] = (2 * ds + (n / 16 + 64) * STEP) * (p @ np.abs(v[h // g]))
+            bound[s, h] = (2 * ds + (n / 16 + 64) * STEP) * (p @ np.abs(v[h // g])) \
+                + n * 2.0 ** -38 * np.abs(v[h // g]).max()
     return out, bound
 
 
