@@ -123,47 +123,63 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done)
   return e;
 }
 
-// Workspace: a record for each warp of the attention kernel, then two parts for each.
+// Column tiles of four query heads that share one pass over the keys and values
+// of their KV head: 1 for groups up to 4, 2 up to 8, else 4; 2 at most for
+// head_dim 256, where q and o of 16 heads are more than the registers hold.
+template <class F>
+cudaError_t with_attn(const ntx_paged_kv* kv, int n_q_heads, F f) {
+  const int G = n_q_heads / kv->n_kv_heads;
+  return with_type(kv->type, [&](auto t) {
+    return with_dim(kv->head_dim, [&](auto d) {
+      if (G <= 4) return f(t, d, std::integral_constant<int, 1>{});
+      if constexpr (decltype(d)::value <= 128)
+        if (G > 8) return f(t, d, std::integral_constant<int, 4>{});
+      return f(t, d, std::integral_constant<int, 2>{});
+    });
+  });
+}
+
+// Workspace: a record of 16 bytes for each warp of the attention kernel, then two parts for each.
 size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
   size_t n = 0;
-  with_type(kv->type, [&](auto t) {
-    return with_dim(kv->head_dim, [&](auto d) {
-      using F = PagedCfg<decltype(t)::value, decltype(d)::value>;
-      const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
-      const int G = n_q_heads / kv->n_kv_heads;
-      n = warps * (sizeof(int4) + 2 * sizeof(float) * paged_part_floats(G < 8 ? G : 8, kv->head_dim));
-      return cudaSuccess;
-    });
+  with_attn(kv, n_q_heads, [&](auto t, auto d, auto nc) {
+    using F = PagedCfg<decltype(t)::value, decltype(d)::value, decltype(nc)::value>;
+    const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
+    const int G = n_q_heads / kv->n_kv_heads;
+    n = warps * (16 + 2 * sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
+    return cudaSuccess;
   });
   return n;
 }
 
-template <int T, int D>
+template <int T, int D, int NC>
 cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
                               const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
-  using F = PagedCfg<T, D>;
+  using F = PagedCfg<T, D, NC>;
   static std::atomic<unsigned long long> done{0}, done_join{0};
-  const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS;
-  int4* splits = static_cast<int4*>(ws);
-  float* part = reinterpret_cast<float*>(splits + warps);
-  cudaError_t e = allow_smem(attn_paged_kernel<T, D>, F::SMEM, done);
+  const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS, G = Hq / kv.n_kv_heads;
+  // records of 4 and 8 bytes, then the parts, 16-byte aligned
+  int* splits = static_cast<int*>(ws);
+  int2* split_at = reinterpret_cast<int2*>(splits + warps);
+  float* part = reinterpret_cast<float*>(splits + 4 * (size_t)warps);
+  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC>, F::SMEM, done);
   if (e == cudaSuccess) e = allow_smem(attn_paged_join_kernel<D>, 64 * 1024, done_join);
   if (e != cudaSuccess) return e;
-  attn_paged_kernel<T, D><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, splits, part, Hq, lens, scale,
-                                                                   device_status_ptr());
+  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, splits, split_at, part, Hq, lens,
+                                                                   scale, device_status_ptr());
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sm_count() * 4);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = warps * sizeof(int4);
+  cfg.dynamicSmemBytes = warps * sizeof(int2);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int4*)splits, warps, (const float*)part, out, Hq,
-                            (int)kv.n_kv_heads);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int*)splits, (const int2*)split_at, warps,
+                            (const float*)part, out, Hq, G, G < F::HEADS ? G : F::HEADS);
 }
 
 int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }
@@ -268,11 +284,9 @@ int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stri
     return failf(NTX_ERR_INVALID_ARG, "%s: out overlaps q", who);
   if (ws_bytes < ntx_attn_paged_workspace_bytes(kv, n_q_heads))
     return failf(NTX_ERR_NOMEM, "%s: workspace too small", who);
-  return finish(who, with_type(kv->type, [&](auto t) {
-    return with_dim(kv->head_dim, [&](auto d) {
-      return launch_attn_paged<decltype(t)::value, decltype(d)::value>(*kv, q, q_stride, out, n_q_heads, ctx_lens,
-                                                                       scale, workspace, (cudaStream_t)stream);
-    });
+  return finish(who, with_attn(kv, n_q_heads, [&](auto t, auto d, auto nc) {
+    return launch_attn_paged<decltype(t)::value, decltype(d)::value, decltype(nc)::value>(
+        *kv, q, q_stride, out, n_q_heads, ctx_lens, scale, workspace, (cudaStream_t)stream);
   }));
 }
 

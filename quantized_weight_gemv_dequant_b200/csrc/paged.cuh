@@ -2,6 +2,8 @@
 // the cache's write and read-back, and decode attention over it.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "ntx.h"
 
@@ -222,22 +224,26 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const float* q, const
 //
 //   out[s][h] = sum_p softmax_p(scale q.k_p) v_p       (p < len[s])
 //
-// A warp works on items (sequence, KV head, tile of up to 8 of its query heads)
+// A warp works on items (sequence, KV head, tile of up to 4 NC of its query heads)
 // in chunks of CH positions, with m16n8k16 fp16 matrix instructions and one pass
 // over the data: running maximum m (base 2), sum l and output o of a softmax.
+// Keys (16 positions) and values (16 elements) are the instruction's A, q and p
+// its B of 8 columns.
 //
-// fp32 accuracy from fp16 products: a tile has at most 8 query heads, so the
-// lower 8 of the instruction's 16 rows are free.  Row g holds the upper 11 bits
-// of head g's operand, row g + 8 the rounded remainder; both land in the same
-// thread's accumulators (c0, c1 and c2, c3) and are added there: 22 bits of q
-// and p at no extra instruction.  Keys and values are exact in fp16: F16 as
-// they are, the codes of block types as integers.  A key block's scale
-// multiplies its partial score in fp32; a value block's scale multiplies p
-// before p is split.  q is first scaled by a power of two that puts its largest
-// element in [2^13, 2^14), p times the scales likewise for each chunk, so
-// neither overflows fp16 and the remainders lose nothing to its subnormals.
-// The matrix instruction's fp32 accumulation truncates, so it only sums one
-// block (keys) or one chunk (values); longer sums are ordinary fp32 adds.
+// fp32 accuracy from fp16 products: columns 2h and 2h + 1 of a tile belong to head
+// h, one with the upper 11 bits of its operand, the other with the rounded
+// remainder; both products land in one thread's accumulators and are added there:
+// 22 bits of q and p.  Keys and values are exact in fp16: F16 as they are, the
+// codes of block types as integers.  A key block's scale multiplies its partial
+// score in fp32; a value block's scale multiplies p, again as two fp16 numbers
+// (the product of the upper parts, what its rounding leaves, and the product of
+// the lower part).  q is first scaled by a power of two that puts its largest
+// element in [2^13, 2^14); p is kept 2^14 fold (F16) or 2^10 fold, and value
+// scales times a power of two that puts the chunk's largest in [2^4, 2^5): nothing
+// overflows fp16, and what its subnormals round off is below 2^-35 of the largest
+// weight and 2^-29 of the chunk's largest value.
+// The matrix instruction's fp32 accumulation truncates, so it only sums one block
+// (keys) or one chunk (values); longer sums are ordinary fp32 adds.
 //
 // Work: the chunks of all items in a row, cut into equal parts, one per warp of
 // a grid that fills the GPU, whatever the lengths.  A part that holds a whole
@@ -246,7 +252,10 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const float* q, const
 // shared-memory slots with 16-byte asynchronous copies, across items, without a
 // barrier.  The order of every sum is fixed by lengths and grid.
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid_bytes) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, int valid_bytes) {  // then zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid_bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -276,12 +285,29 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t r[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8x8 matrix of 16-bit elements, a row in 4 lanes
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm2_trans(uint32_t a, uint32_t r[2]) {  // two: addresses of lanes 0-15
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a));
+}
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  float d0, d1, d2, d3;
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d0), "=f"(d1), "=f"(d2), "=f"(d3)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+  c[0] = d0; c[1] = d1; c[2] = d2; c[3] = d3;
+}
+__device__ __forceinline__ void mma16816_first(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -314,21 +340,21 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x) {
                          bits_h2(0xD480D480u)));  // (1024 + 16 q) / 16 - 72
 }
 
-// Positions per chunk, ring slots (one K or V chunk each) and warps.  Eight warps
-// per SM carry three 8 KiB slots each of F16; block types are smaller and spend
-// more instructions per byte, so they take sixteen warps where 128 registers do.
-template <int T, int D>
+// Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.
+template <int T, int D, int NC>
 struct PagedCfg {
   static constexpr int CH = (T == kKvF16 && D == 256) ? 16 : 32;
   static constexpr int SLOTS = (T == kKvF16 || (T == kKvQ8 && D >= 128)) ? 3 : 4;
-  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : 4;
+  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 128 ? 4 : D * NC <= 256 ? 3 : 2;
+  static constexpr int HEADS = 4 * NC;                     // query heads of a tile
   static constexpr int WARPS = 4;
-  static constexpr int CB = kv_code_bytes<T>(D);          // bytes of a row's codes
+  static constexpr int CB = kv_code_bytes<T>(D);           // bytes of a row's codes
   static constexpr int SB = T == kKvF16 ? 0 : D / 16;      // bytes of a row's scales
   static constexpr int SLOT = CH * (CB + SB);
   static constexpr int SMEM = WARPS * SLOTS * SLOT;
 };
-__host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * 8; }
+constexpr int kMaxTile = 16;  // heads of a tile at most: a part is m[16], l[16], o[heads][D]
+__host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * kMaxTile; }
 
 // Position of 16-byte column `col` of a slot row, so that eight consecutive rows
 // of one column lie in different banks.
@@ -352,19 +378,42 @@ __device__ __forceinline__ int seq_len(const ntx_paged_kv& c, const int* lens, i
   return n < 0 ? 0 : most;
 }
 
-// A place in the row of all chunks: chunk `ci` of `n` of tile `tile` of sequence `s`.
+// A place in the row of all chunks: chunk `ci` of `n` of row tile `rt` of KV head
+// `kvh` of sequence `s`.
 struct PagedCursor {
-  int s, tile, ci, n, len;
-  __device__ __forceinline__ void next(const ntx_paged_kv& c, const int* lens, int tiles, int ch, int* status) {
-    if (++ci < n) return;
+  int s, kvh, rt, ci, n, len;
+  // to the next chunk; true where it is the first of an item
+  __device__ __forceinline__ bool next(const ntx_paged_kv& c, const int* lens, int rtiles, int ch, int* status) {
+    if (++ci < n) return false;
     ci = 0;
-    if (++tile < tiles) return;
-    tile = 0;
+    if (++rt < rtiles) return true;
+    rt = 0;
+    if (++kvh < c.n_kv_heads) return true;
+    kvh = 0;
     do {
-      if (++s >= c.n_seqs) { n = 0; return; }
+      if (++s >= c.n_seqs) { n = 0; return true; }
       len = seq_len(c, lens, s, status);
       n = (len + ch - 1) / ch;
     } while (n == 0);
+    return true;
+  }
+};
+
+// W chunks in consecutive parts for at most `warps` warps, sizes differing by one at most.
+struct PagedParts {
+  int n;
+  int64_t size, longer;  // the first `longer` parts have size + 1 chunks
+  __device__ __forceinline__ PagedParts(int64_t W, int warps) : n((int)min64(W, warps)), size(0), longer(0) {
+    if (n == 0) return;
+    size = W >> 31 ? W / n : (int)W / n;
+    longer = W - size * n;
+  }
+  __device__ __forceinline__ int64_t begin(int w) const { return w * size + min64(w, longer); }
+  __device__ __forceinline__ int holder(int64_t chunk) const {
+    const int64_t head = longer * (size + 1);
+    if (chunk < head) return (int)(chunk >> 31 ? chunk / (size + 1) : (int)chunk / (int)(size + 1));
+    chunk -= head;
+    return (int)(longer + (chunk >> 31 ? chunk / size : (int)chunk / (int)size));
   }
 };
 
@@ -381,17 +430,18 @@ __device__ __forceinline__ int64_t lane_chunks(const ntx_paged_kv& c, const int*
   return sum;
 }
 
-template <int T, int D>
-__global__ void __launch_bounds__(128, PagedCfg<T, D>::CTAS)
+template <int T, int D, int NC>
+__global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     attn_paged_kernel(const ntx_paged_kv c, const float* __restrict__ q, int64_t qs, float* __restrict__ out,
-                      int4* __restrict__ splits, float* __restrict__ part, int Hq, const int* __restrict__ lens,
-                      float scale, int* status) {
-  using F = PagedCfg<T, D>;
-  constexpr int CH = F::CH, C = F::CB / 16, NB = D / 32, NJ = CH / 8, NS = CH / 16, NT = D / 8;
+                      int* __restrict__ splits, int2* __restrict__ split_at, float* __restrict__ part, int Hq,
+                      const int* __restrict__ lens, float scale, int* status) {
+  using F = PagedCfg<T, D, NC>;
+  constexpr int CH = F::CH, C = F::CB / 16, NB = D / 32, NS = CH / 16, NT = D / 16;
   extern __shared__ __align__(128) uint8_t ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t slots = smem_addr(ring) + warp * (F::SLOTS * F::SLOT);
-  const int G = Hq / c.n_kv_heads, rtiles = (G + 7) >> 3, tiles = c.n_kv_heads * rtiles;
+  const int G = Hq / c.n_kv_heads, rtiles = (G + F::HEADS - 1) / F::HEADS;
+  const int tiles = c.n_kv_heads * rtiles;
   const int wid = warp * gridDim.x + blockIdx.x, all_warps = gridDim.x * F::WARPS;
 
   // empty sequences: zeros
@@ -414,13 +464,13 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D>::CTAS)
       if (lane >= o) upto += v;
     }
     const int64_t W = __shfl_sync(0xffffffffu, upto, 31);
-    const int64_t n_warps = min64(all_warps, W);  // none without a chunk
-    if (wid >= n_warps) {
-      if (lane == 0) splits[wid] = make_int4(0, 0, 0, 0);
+    const PagedParts parts_of(W, all_warps);
+    if (wid >= parts_of.n) {
+      if (lane == 0) splits[wid] = 0;
       return;
     }
-    const int64_t c0 = wid * W / n_warps;
-    todo = (wid + 1) * W / n_warps - c0;
+    const int64_t c0 = parts_of.begin(wid);
+    todo = parts_of.begin(wid + 1) - c0;
     const int at = __ffs(__ballot_sync(0xffffffffu, upto > c0)) - 1;  // the lane whose sequences hold c0
     int64_t rest = c0 - __shfl_sync(0xffffffffu, upto - mine, at);
     cur.s = at * k;
@@ -431,368 +481,462 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D>::CTAS)
       rest -= (int64_t)cur.n * tiles;
       ++cur.s;
     }
-    cur.tile = (int)(rest / cur.n);
-    cur.ci = (int)(rest - (int64_t)cur.tile * cur.n);
+    const int tile = (int)(rest / cur.n);
+    cur.ci = (int)(rest - (int64_t)tile * cur.n);
+    cur.kvh = tile / rtiles;
+    cur.rt = tile - cur.kvh * rtiles;
     item_head = cur.ci == 0;
     // The first warp that begins inside an item describes it for the join: its
     // parts lie in slot 1 of the warp before and slot 0 of this and the next ones.
     if (lane == 0) {
       const int64_t first = c0 - cur.ci;
       int parts = 0;
-      if (!item_head && (wid - 1) * W / n_warps <= first) parts = (int)(((first + cur.n) * n_warps - 1) / W) - wid + 2;
-      splits[wid] = make_int4(parts, wid - 1, cur.s, cur.tile);
+      if (!item_head && parts_of.begin(wid - 1) <= first) parts = parts_of.holder(first + cur.n - 1) - wid + 2;
+      splits[wid] = parts;
+      split_at[wid] = make_int2(cur.s, cur.kvh * G + F::HEADS * cur.rt);
     }
   }
 
-  // ---- loading: the ring's next slot takes K, then V, of chunk `ld`
-  const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D);
+  // ---- loading: the ring's next slot takes K or V of chunk `ld`, 16 rows (one page) at a time
+  const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D), scales_at = (int64_t)c.page_size * F::CB;
   PagedCursor ld = cur;
   int64_t ld_left = todo;
-  int ld_slot = 0;
-  bool ld_v = false;
-  int ld_page[NS], ld_row[NS];
-  auto look_up = [&]() {
+  uint32_t ld_slot = slots;
+  int ld_j, ld_row, ld_page[NS], ld_first[NS];  // next page index and row in it; pages and first rows of chunk `ld`
+  auto look_up = [&](bool item) {
+    if (item) {
+      ld_j = ld.ci * CH / c.page_size;
+      ld_row = ld.ci * CH - ld_j * c.page_size;
+    }
+    const int* row = c.page_table + (int64_t)ld.s * c.max_pages;
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
-      const int pos = ld.ci * CH + 16 * r, j = pos / c.page_size;
-      ld_row[r] = pos - j * c.page_size;
-      ld_page[r] = pos < ld.len ? __ldg(c.page_table + (int64_t)ld.s * c.max_pages + j) : -1;
+      ld_first[r] = ld_row;
+      ld_page[r] = ld.ci * CH + 16 * r < ld.len ? __ldg(row + ld_j) : -1;
+      if ((ld_row += 16) == c.page_size) {
+        ld_row = 0;
+        ++ld_j;
+      }
     }
   };
-  look_up();
-  auto load = [&]() {
+  look_up(true);
+  // This lane's 16-byte pieces of 16 rows of C columns: row i (32/C) + lane/C, column
+  // lane % C; i changes only bits 4 to 6 of the swizzled place besides its row's start.
+  const uint32_t lane_off = lane * 16;
+  const uint32_t lane_k = lane / C * F::CB + swz_k<T, C>(lane / C, lane % C) * 16;
+  const uint32_t lane_v = lane / C * F::CB + swz8<C>(lane / C, lane % C) * 16;
+  int64_t ld_at[NS];  // byte offset of this lane's first piece in either pool
+  int ld_rows[NS];    // rows to copy, the others are zeros
+  auto load = [&](auto is_v) {
+    constexpr bool V = decltype(is_v)::value;
     if (ld_left > 0) {
-      const uint8_t* pool = static_cast<const uint8_t*>(ld_v ? c.v_pages : c.k_pages);
-      const uint32_t slot = slots + ld_slot * F::SLOT;
-      const int kvh = ld.tile / rtiles;
+      const uint8_t* pool = static_cast<const uint8_t*>(V ? c.v_pages : c.k_pages);
 #pragma unroll
       for (int r = 0; r < NS; ++r) {
-        int left = ld.len - (ld.ci * CH + 16 * r);  // rows of this group that the sequence has
-        if (left > 0 && (unsigned)ld_page[r] >= (unsigned)c.n_pages) {
-          if (lane == 0) bad_page(status);
-          left = 0;
+        if constexpr (!V) {
+          int rows = ld.len - (ld.ci * CH + 16 * r), page = ld_page[r];
+          if (rows > 0 && (unsigned)page >= (unsigned)c.n_pages) {
+            if (lane == 0) bad_page(status);
+            rows = 0;
+          }
+          if (rows <= 0) page = 0;
+          ld_rows[r] = rows;
+          ld_at[r] = ((int64_t)page * c.n_kv_heads + ld.kvh) * head_bytes + lane_off;
         }
-        const uint8_t* src = left > 0 ? pool + ((int64_t)ld_page[r] * c.n_kv_heads + kvh) * head_bytes : pool;
-        const uint8_t* codes = left > 0 ? src + (int64_t)ld_row[r] * F::CB : src;
+        const uint8_t* codes = pool + ld_at[r] + ld_first[r] * F::CB;
+        const uint8_t* sc = pool + ld_at[r] + (scales_at + ld_first[r] * F::SB);
+        const uint32_t dst = ld_slot + 16 * r * F::CB + (V ? lane_v : lane_k);
+        const uint32_t dst_sc = ld_slot + CH * F::CB + r * 16 * F::SB + lane_off;
+        auto place = [&](int i) {
+          constexpr int RPI = C >= 32 ? 1 : 32 / C;  // rows per i
+          return (dst ^ ((V ? swz8<C>(i * RPI, 0) : swz_k<T, C>(i * RPI, 0)) * 16)) + i * RPI * F::CB;
+        };
+        if (ld_rows[r] >= 16) {
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {  // 16 rows of C columns, 32 lanes
-          const int idx = i * 32 + lane, row = idx / C, col = idx % C;
-          const int pc = ld_v ? swz8<C>(row, col) : swz_k<T, C>(row, col);
-          const bool on = row < left;
-          cp_async16(slot + (16 * r + row) * F::CB + pc * 16, on ? codes + idx * 16 : pool, on ? 16 : 0);
-        }
-        if constexpr (F::SB > 0) {
-          if (lane < F::SB) {  // 16 rows of SB bytes
-            const int valid = max(0, min(16, left * F::SB - lane * 16));
-            const uint8_t* sc = src + (int64_t)c.page_size * F::CB + (int64_t)ld_row[r] * F::SB + lane * 16;
-            cp_async16(slot + CH * F::CB + r * 16 * F::SB + lane * 16, valid ? sc : pool, valid);
+          for (int i = 0; i < C / 2; ++i) cp_async16(place(i), codes + i * 512);
+          if (F::SB > 0 && lane < F::SB) cp_async16(dst_sc, sc);
+        } else {
+#pragma unroll
+          for (int i = 0; i < C / 2; ++i) {
+            const bool on = i * (32 / C) + lane / C < ld_rows[r];
+            cp_async16_fill(place(i), on ? codes + i * 512 : pool, on ? 16 : 0);
+          }
+          if (F::SB > 0 && lane < F::SB) {
+            const int valid = max(0, min(16, ld_rows[r] * F::SB - lane * 16));
+            cp_async16_fill(dst_sc, valid ? sc : pool, valid);
           }
         }
       }
-      ld_slot = ld_slot + 1 == F::SLOTS ? 0 : ld_slot + 1;
-      if (ld_v) {
-        if (--ld_left > 0) {
-          ld.next(c, lens, tiles, CH, status);
-          look_up();  // used when the next K is loaded, half a chunk from now
-        }
+      ld_slot = ld_slot + F::SLOT == slots + F::SLOTS * F::SLOT ? slots : ld_slot + F::SLOT;
+      if constexpr (V) {
+        // the pages of the next chunk are used half a chunk from now
+        if (--ld_left > 0) look_up(ld.next(c, lens, rtiles, CH, status));
       }
-      ld_v = !ld_v;
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < F::SLOTS - 1; ++i) load();
+  uint32_t slot = slots;
+  auto next_slot = [&]() { slot = slot + F::SLOT == slots + F::SLOTS * F::SLOT ? slots : slot + F::SLOT; };
+  constexpr std::false_type kK{};
+  constexpr std::true_type kV{};
+  load(kK);
+  load(kV);
+  if constexpr (F::SLOTS == 4) load(kK);
+  // what is loaded while K / V of a chunk is used: SLOTS - 1 slots ahead
+  constexpr std::bool_constant<F::SLOTS == 4> with_k{};
+  constexpr std::bool_constant<F::SLOTS == 3> with_v{};
+  static_assert(F::SLOTS == 3 || F::SLOTS == 4);
 
-  // scales of rows 8 j + 2 t and the next one, as pairs of blocks
-  auto scales = [&](uint32_t slot, int j, uint32_t sc[NB]) {
-    const uint32_t a = slot + CH * F::CB + (8 * j + 2 * t) * F::SB;
+  // scales of a row, two blocks a word
+  auto scales = [&](uint32_t row, uint32_t sc[NB / 2]) {
+    const uint32_t a = slot + CH * F::CB + row * F::SB;
     if constexpr (NB == 2) {
+      sc[0] = lds32(a);
+    } else if constexpr (NB == 4) {
       const uint2 v = lds64(a);
       sc[0] = v.x; sc[1] = v.y;
     } else {
-#pragma unroll
-      for (int i = 0; i < NB / 4; ++i) {
-        const uint4 v = lds128(a + 16 * i);
-        sc[4 * i] = v.x; sc[4 * i + 1] = v.y; sc[4 * i + 2] = v.z; sc[4 * i + 3] = v.w;
-      }
+      const uint4 v = lds128(a);
+      sc[0] = v.x; sc[1] = v.y; sc[2] = v.z; sc[3] = v.w;
     }
   };
-  // of those, the scale of row `odd` and block b
-  auto scale_of = [](const uint32_t sc[NB], int odd, int b) {
-    const uint32_t u = sc[odd * (NB / 2) + b / 2];
-    return half_bits_to_float((b & 1) ? u >> 16 : u);
-  };
 
-  uint32_t qf[2 * NB][4];
-  float o[NT][2], m = 0.f, l = 0.f, to_log2 = 0.f;
-  int slot_i = 0;
+  // p is kept 2^kPBits fold, in l and o too
+  constexpr float kPBits = T == kKvF16 ? 14.f : 10.f;
+  // Block types' keys enter the products as fp16 subnormals, (code + offset) 2^-24
+  constexpr float kCodeUnit = T == kKvF16 ? 1.f : 16777216.f;
+  // This lane's heads: t of column tile c as a softmax row (with positions g, g + 8 of 16)
+  // and in o (with two elements of 16); g / 2 in q's fragments.
+  uint32_t qf[NC][NB][4];
+  float o[NC][NT][2], m[NC], l[NC], to_log2[NC];
+  float off[NC][NB];  // block types: the offset's share of a block's product
   bool fresh = true;
+  int rows = 0, head0 = 0;
 
   for (;;) {
     // ---- scores
     cp_async_wait<F::SLOTS - 2>();
     __syncwarp();
-    load();
-    const int kvh = cur.tile / rtiles, rt = cur.tile - kvh * rtiles;
-    const int rows = min(8, G - 8 * rt), head0 = kvh * G + 8 * rt;
+    load(with_k);
     if (fresh) {
-      float x[NB][8], top = 0.f;
-      const float* qp = q + cur.s * qs + (int64_t)(head0 + g) * D;
+      rows = min(F::HEADS, G - F::HEADS * cur.rt);
+      head0 = cur.kvh * G + F::HEADS * cur.rt;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-        if (g < rows) {
-          if constexpr (T == kKvQ4) {
-            u = ldg4(qp + 32 * b + 4 * t);
-            v = ldg4(qp + 32 * b + 16 + 4 * t);
-          } else {
-            u = ldg4(qp + 32 * b + 8 * t);
-            v = ldg4(qp + 32 * b + 8 * t + 4);
+      for (int ct = 0; ct < NC; ++ct) {
+        const int h = 4 * ct + (g >> 1);
+        const float* qp = q + cur.s * qs + (int64_t)(head0 + h) * D;
+        float x[NB][8], top = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+          if (h < rows) {
+            u = ldg4(qp + 32 * b + (T == kKvQ4 ? 4 * t : 8 * t));
+            v = ldg4(qp + 32 * b + (T == kKvQ4 ? 16 + 4 * t : 8 * t + 4));
+          }
+          x[b][0] = u.x; x[b][1] = u.y; x[b][2] = u.z; x[b][3] = u.w;
+          x[b][4] = v.x; x[b][5] = v.y; x[b][6] = v.z; x[b][7] = v.w;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e with top 2^e in [2^13, 2^14), as far as fp32 has it; 1 for infinities
+        const int eb = __float_as_int(top) >> 23;
+        const int es = eb == 255 ? 127 : min(254, 267 - eb);
+        const float up = __int_as_float(es << 23);
+        const float down = es == 254 ? __int_as_float(0x00400000) : __int_as_float((254 - es) << 23);
+        to_log2[ct] = __shfl_sync(0xffffffffu, scale * down * (1.44269504088896340736f * kCodeUnit), 8 * t);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // the pairs that a key fragment of this type has: elements 0 1, 2 3, ... or 0 2, 1 3, ... of
+            // this lane's; a high nibble counts 16 fold
+            const int i0 = T == kKvQ4 ? 4 * (i >> 1) + (i & 1) : 2 * i, i1 = T == kKvQ4 ? i0 + 2 : i0 + 1;
+            const float w = T == kKvQ4 && i >= 2 ? 0.0625f : 1.f;
+            uint32_t hi, lo;
+            split2(x[b][i0] * up * w, x[b][i1] * up * w, hi, lo);
+            qf[ct][b][i] = (g & 1) ? lo : hi;
+            const float2 f = __half22float2(bits_h2(qf[ct][b][i]));
+            sum = fmaf(f.x + f.y, 1.f / w, sum);
+          }
+          if constexpr (T != kKvF16) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sum = __shfl_sync(0xffffffffu, sum, 8 * t) + __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            off[ct][b] = sum * (-(T == kKvQ4 ? 8.f : 128.f) / kCodeUnit);
           }
         }
-        x[b][0] = u.x; x[b][1] = u.y; x[b][2] = u.z; x[b][3] = u.w;
-        x[b][4] = v.x; x[b][5] = v.y; x[b][6] = v.z; x[b][7] = v.w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
+        for (int n = 0; n < NT; ++n) o[ct][n][0] = o[ct][n][1] = 0.f;
+        m[ct] = -INFINITY;
+        l[ct] = 0.f;
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^e with top 2^e in [2^13, 2^14), as far as fp32 has it; 1 for infinities
-      const int eb = __float_as_int(top) >> 23;
-      const int es = eb == 255 ? 127 : min(254, 267 - eb);
-      const float up = __int_as_float(es << 23);
-      const float down = es == 254 ? __int_as_float(0x00400000) : __int_as_float((254 - es) << 23);
-      to_log2 = scale * down * 1.44269504088896340736f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float* y = x[b] + 4 * h;
-          // the pairing that the K fragments of this type have
-          const int i1 = T == kKvQ4 ? 2 : 1, i2 = T == kKvQ4 ? 1 : 2;
-          split2(y[0] * up, y[i1] * up, qf[2 * b + h][0], qf[2 * b + h][1]);
-          split2(y[i2] * up, y[3] * up, qf[2 * b + h][2], qf[2 * b + h][3]);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = 0.f;
-      m = -INFINITY;
-      l = 0.f;
       fresh = false;
     }
 
-    float s[NJ][2];
-    {
-      const uint32_t slot = slots + slot_i * F::SLOT;
-      if constexpr (T == kKvF16) {
-        float acc[NJ][4];
+    float s[NC][NS][2];
+    if constexpr (T == kKvF16) {
+      float acc[NC][NS][4];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int k = 0; k < NS; ++k) {
+          const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, 4 * b + t) * 16;
+          const uint4 u = lds128(a), v = lds128(a + 8 * F::CB);
+          const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const uint4 k = lds128(slot + (8 * j + g) * F::CB + swz_k<T, C>(g, 4 * b + t) * 16);
-            mma16816(acc[j], qf[2 * b], k.x, k.y);
-            mma16816(acc[j], qf[2 * b + 1], k.z, k.w);
+          for (int ct = 0; ct < NC; ++ct) {
+            if (b == 0) mma16816_first(acc[ct][k], a0, qf[ct][b][0], qf[ct][b][1]);
+            else mma16816(acc[ct][k], a0, qf[ct][b][0], qf[ct][b][1]);
+            mma16816(acc[ct][k], a1, qf[ct][b][2], qf[ct][b][3]);
+          }
+        }
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          s[ct][k][0] = acc[ct][k][0] + acc[ct][k][1];
+          s[ct][k][1] = acc[ct][k][2] + acc[ct][k][3];
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        uint32_t sc[2][NB / 2];
+        scales(16 * k + g, sc[0]);
+        scales(16 * k + g + 8, sc[1]);
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct) s[ct][k][0] = s[ct][k][1] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t a0[4], a1[4];
+          if constexpr (T == kKvQ8) {
+            const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, 2 * b + (t >> 1)) * 16 + (t & 1) * 8;
+            uint2 u = lds64(a), v = lds64(a + 8 * F::CB);
+            u.x ^= 0x80808080u; u.y ^= 0x80808080u; v.x ^= 0x80808080u; v.y ^= 0x80808080u;
+            a0[0] = __byte_perm(u.x, 0, 0x4140); a0[1] = __byte_perm(v.x, 0, 0x4140);
+            a0[2] = __byte_perm(u.x, 0, 0x4342); a0[3] = __byte_perm(v.x, 0, 0x4342);
+            a1[0] = __byte_perm(u.y, 0, 0x4140); a1[1] = __byte_perm(v.y, 0, 0x4140);
+            a1[2] = __byte_perm(u.y, 0, 0x4342); a1[3] = __byte_perm(v.y, 0, 0x4342);
+          } else {
+            const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, b) * 16 + 4 * t;
+            const uint32_t u = lds32(a), v = lds32(a + 8 * F::CB), u8 = u >> 8, v8 = v >> 8;
+            a0[0] = u & 0x000F000Fu; a0[1] = v & 0x000F000Fu; a0[2] = u8 & 0x000F000Fu; a0[3] = v8 & 0x000F000Fu;
+            a1[0] = u & 0x00F000F0u; a1[1] = v & 0x00F000F0u; a1[2] = u8 & 0x00F000F0u; a1[3] = v8 & 0x00F000F0u;
+          }
+          float d[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 f = __half22float2(bits_h2(sc[i][b / 2]));
+            d[i] = (b & 1) ? f.y : f.x;
           }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          s[j][0] = acc[j][0] + acc[j][2];
-          s[j][1] = acc[j][1] + acc[j][3];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          uint32_t sc[NB];
-          scales(slot, j, sc);
-          s[j][0] = s[j][1] = 0.f;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (T == kKvQ8) {
-              uint2 k = lds64(slot + (8 * j + g) * F::CB + swz_k<T, C>(g, 2 * b + (t >> 1)) * 16 + (t & 1) * 8);
-              k.x ^= 0x80808080u;
-              k.y ^= 0x80808080u;
-              mma16816(acc, qf[2 * b], bytes_h2<0x4140>(k.x), bytes_h2<0x4342>(k.x));
-              mma16816(acc, qf[2 * b + 1], bytes_h2<0x4140>(k.y), bytes_h2<0x4342>(k.y));
-            } else {
-              const uint32_t k = lds32(slot + (8 * j + g) * F::CB + swz_k<T, C>(g, b) * 16 + 4 * t), k8 = k >> 8;
-              mma16816(acc, qf[2 * b], nib_lo(k), nib_lo(k8));
-              mma16816(acc, qf[2 * b + 1], nib_hi(k), nib_hi(k8));
-            }
-            s[j][0] = fmaf(acc[0] + acc[2], scale_of(sc, 0, b), s[j][0]);
-            s[j][1] = fmaf(acc[1] + acc[3], scale_of(sc, 1, b), s[j][1]);
+          for (int ct = 0; ct < NC; ++ct) {
+            float acc[4];
+            mma16816_first(acc, a0, qf[ct][b][0], qf[ct][b][1]);
+            mma16816(acc, a1, qf[ct][b][2], qf[ct][b][3]);
+            s[ct][k][0] = fmaf(acc[0] + acc[1] + off[ct][b], d[0], s[ct][k][0]);
+            s[ct][k][1] = fmaf(acc[2] + acc[3] + off[ct][b], d[1], s[ct][k][1]);
           }
         }
       }
-      slot_i = slot_i + 1 == F::SLOTS ? 0 : slot_i + 1;
     }
+    next_slot();
 
     // ---- softmax of the chunk
     const int left = cur.len - cur.ci * CH;  // positions the chunk has
-    float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int ct = 0; ct < NC; ++ct) {
+      float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[j][i] *= to_log2;
-        if (left < CH && 8 * j + 2 * t + i >= left) s[j][i] = -INFINITY;
-        top = fmaxf(top, s[j][i]);
-      }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.f : m_new;
-    const float fade = ex2(m - base);
-    m = m_new;
-    l *= fade;
+      for (int k = 0; k < NS; ++k)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+        for (int i = 0; i < 2; ++i) {
+          s[ct][k][i] *= to_log2[ct];
+          if (left < CH && 16 * k + 8 * i + g >= left) s[ct][k][i] = -INFINITY;  // behind the sequence
+          top = fmaxf(top, s[ct][k][i]);
+        }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[j][i] = ex2(s[j][i] - base);
-        l += s[j][i];
-      }
-    if (__any_sync(0xffffffffu, fade != 1.f)) {
+      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float m_new = fmaxf(m[ct], top), zero = m_new == -INFINITY ? 0.f : m_new, base = zero - kPBits;
+      const float fade = ex2(m[ct] - zero);
+      m[ct] = m_new;
+      l[ct] *= fade;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][0] *= fade;
-        o[n][1] *= fade;
+      for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s[ct][k][i] = ex2(s[ct][k][i] - base);
+          l[ct] += s[ct][k][i];
+        }
+      if (__any_sync(0xffffffffu, fade != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[ct][n][0] *= fade;
+          o[ct][n][1] *= fade;
+        }
       }
     }
 
     // ---- weighted values
     cp_async_wait<F::SLOTS - 2>();
     __syncwarp();
-    load();
-    {
-      const uint32_t slot = slots + slot_i * F::SLOT;
-      // ldmatrix rows: lanes 0-7 and 8-15 the two halves of 16 positions, 16-31 the next column
-      const int lr = lane & 15, lc = lane >> 4;
-      if constexpr (T == kKvF16) {
-        uint32_t p[NS][4];
+    load(with_v);
+    if constexpr (T == kKvF16) {
+      uint32_t p[NC][NS][2];
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct)
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-          split2(s[2 * k][0] * 16384.f, s[2 * k][1] * 16384.f, p[k][0], p[k][1]);
-          split2(s[2 * k + 1][0] * 16384.f, s[2 * k + 1][1] * 16384.f, p[k][2], p[k][3]);
+          uint32_t hi, lo;
+          split2(s[ct][k][0], s[ct][k][1], hi, lo);
+          p[ct][k][0] = transpose8(__byte_perm(hi, lo, 0x5410));
+          p[ct][k][1] = transpose8(__byte_perm(hi, lo, 0x7632));
         }
+      // ldmatrix rows: positions 0-7 of two columns, then 8-15 of them
+      const int lr = (lane & 7) + ((lane >> 4) << 3), lc = (lane >> 3) & 1;
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < NT; ++n) {
+        uint32_t v[NS][4];
 #pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            uint32_t v[4];
-            ldsm4_trans(slot + (16 * k + lr) * F::CB + swz8<C>(lr, n + lc) * 16, v);
-            mma16816(a0, p[k], v[0], v[1]);
-            mma16816(a1, p[k], v[2], v[3]);
-          }
-          const float f = 1.f / 16384.f;
-          o[n][0] = fmaf(a0[0] + a0[2], f, o[n][0]);
-          o[n][1] = fmaf(a0[1] + a0[3], f, o[n][1]);
-          o[n + 1][0] = fmaf(a1[0] + a1[2], f, o[n + 1][0]);
-          o[n + 1][1] = fmaf(a1[1] + a1[3], f, o[n + 1][1]);
-        }
-      } else {
-        uint32_t sc[NJ][NB];
-        __half2 big = __float2half2_rn(0.f);
+        for (int k = 0; k < NS; ++k) ldsm4_trans(slot + (16 * k + lr) * F::CB + swz8<C>(lr, 2 * n + lc) * 16, v[k]);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          scales(slot, j, sc[j]);
+        for (int ct = 0; ct < NC; ++ct) {
+          float a[4];
+          mma16816_first(a, v[0], p[ct][0][0], p[ct][0][1]);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) big = __hmax2(big, __habs2(bits_h2(sc[j][b])));
-        }
-        uint32_t u = h2_bits(big);
-        int e = max(u & 0xFFFFu, u >> 16);
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-        e >>= 10;  // every |scale| < 2^(e - 14), or infinite
-        const float up = __int_as_float((127 + 28 - e) << 23), down = __int_as_float((127 - 28 + e) << 23);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          s[j][0] *= up;
-          s[j][1] *= up;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float a[4][4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) a[n][0] = a[n][1] = a[n][2] = a[n][3] = 0.f;
-#pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            uint32_t p[4];
-            split2(s[2 * k][0] * scale_of(sc[2 * k], 0, b), s[2 * k][1] * scale_of(sc[2 * k], 1, b), p[0], p[1]);
-            split2(s[2 * k + 1][0] * scale_of(sc[2 * k + 1], 0, b), s[2 * k + 1][1] * scale_of(sc[2 * k + 1], 1, b),
-                   p[2], p[3]);
-            if constexpr (T == kKvQ8) {
-              uint32_t v[4];
-              ldsm4_trans(slot + (16 * k + lr) * F::CB + swz8<C>(lr, 2 * b + lc) * 16, v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] ^= 0x80808080u;
-              mma16816(a[0], p, bytes_h2<0x4240>(v[0]), bytes_h2<0x4240>(v[1]));  // even elements of 16
-              mma16816(a[1], p, bytes_h2<0x4341>(v[0]), bytes_h2<0x4341>(v[1]));  // odd ones
-              mma16816(a[2], p, bytes_h2<0x4240>(v[2]), bytes_h2<0x4240>(v[3]));
-              mma16816(a[3], p, bytes_h2<0x4341>(v[2]), bytes_h2<0x4341>(v[3]));
-            } else {
-              uint32_t v[2];
-              asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
-                           : "=r"(v[0]), "=r"(v[1])
-                           : "r"(slot + (16 * k + lr) * F::CB + swz8<C>(lr, b) * 16));
-              const uint32_t w0 = v[0] >> 8, w1 = v[1] >> 8;
-              mma16816(a[0], p, nib_lo(v[0]), nib_lo(v[1]));
-              mma16816(a[1], p, nib_lo(w0), nib_lo(w1));
-              mma16816(a[2], p, nib_hi(v[0]), nib_hi(v[1]));
-              mma16816(a[3], p, nib_hi(w0), nib_hi(w1));
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            o[4 * b + n][0] = fmaf(a[n][0] + a[n][2], down, o[4 * b + n][0]);
-            o[4 * b + n][1] = fmaf(a[n][1] + a[n][3], down, o[4 * b + n][1]);
-          }
+          for (int k = 1; k < NS; ++k) mma16816(a, v[k], p[ct][k][0], p[ct][k][1]);
+          o[ct][n][0] += a[0] + a[1];
+          o[ct][n][1] += a[2] + a[3];
         }
       }
-      slot_i = slot_i + 1 == F::SLOTS ? 0 : slot_i + 1;
+    } else {
+      uint32_t sc[NS][2][NB / 2];
+      __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          scales(16 * k + 8 * i + g, sc[k][i]);
+#pragma unroll
+          for (int b = 0; b < NB / 2; ++b) big = __hmax2(big, __habs2(bits_h2(sc[k][i][b])));
+        }
+      uint32_t u = h2_bits(big);
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) u = h2_bits(__hmax2(bits_h2(u), bits_h2(__shfl_xor_sync(0xffffffffu, u, x))));
+      const int e = (int)max(u & 0xFFFFu, u >> 16) >> 10;
+      // The largest scale is in [2^(e - 15), 2^(e - 14)), subnormal or infinite; times 2^up it
+      // comes to [2^4, 2^5).  What is beyond 2^15 goes to p.
+      const int up = min(15, 19 - e);
+      const float down = __int_as_float((127 - 19 + e) << 23);
+      const __half2 by = bits_h2((uint32_t)(up + 15) * 0x04000400u);
+      __half2 ph[NC][NS], pl[NC][NS];
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          const float f = e < 4 ? __int_as_float((127 + 4 - e) << 23) : 1.f;
+          uint32_t hi, lo;
+          split2(s[ct][k][0] * f, s[ct][k][1] * f, hi, lo);
+          ph[ct][k] = bits_h2(hi);
+          pl[ct][k] = bits_h2(lo);
+        }
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < NB / 2; ++b) sc[k][i][b] = h2_bits(__hmul2(bits_h2(sc[k][i][b]), by));
+      const int lr = lane & 15, lc = lane >> 4;  // ldmatrix rows: 16 positions, then those of the next column
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float a[NC][2][4];
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          // value fragments: rows g and g + 8 are elements 2 g and 2 g + 1 of 16
+          uint32_t v[2][4];
+          if constexpr (T == kKvQ8) {
+            uint32_t r[4];
+            ldsm4_trans(slot + (16 * k + lr) * F::CB + swz8<C>(lr, 2 * b + lc) * 16, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              r[i] ^= 0x80808080u;
+              v[i >> 1][2 * (i & 1)] = bytes_h2<0x4240>(r[i]);
+              v[i >> 1][2 * (i & 1) + 1] = bytes_h2<0x4341>(r[i]);
+            }
+          } else {
+            uint32_t r[2];
+            ldsm2_trans(slot + (16 * k + lr) * F::CB + swz8<C>(lr, b) * 16, r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t r8 = r[i] >> 8;
+              v[0][2 * i] = nib_lo(r[i]);
+              v[0][2 * i + 1] = nib_lo(r8);
+              v[1][2 * i] = nib_hi(r[i]);
+              v[1][2 * i + 1] = nib_hi(r8);
+            }
+          }
+          const __half2 d = bits_h2(__byte_perm(sc[k][0][b / 2], sc[k][1][b / 2], (b & 1) ? 0x7632 : 0x5410));
+#pragma unroll
+          for (int ct = 0; ct < NC; ++ct) {
+            // p d of positions g, g + 8, in two numbers again
+            const __half2 hi = __hmul2(ph[ct][k], d);
+            const __half2 rest = __hfma2(ph[ct][k], d, __hneg2(hi));  // exact
+            const uint32_t x = h2_bits(hi), y = h2_bits(__hfma2(pl[ct][k], d, rest));
+            const uint32_t p0 = transpose8(__byte_perm(x, y, 0x5410)), p1 = transpose8(__byte_perm(x, y, 0x7632));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (k == 0) mma16816_first(a[ct][i], v[i], p0, p1);
+              else mma16816(a[ct][i], v[i], p0, p1);
+            }
+          }
+        }
+#pragma unroll
+        for (int ct = 0; ct < NC; ++ct)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o[ct][2 * b + i][0] = fmaf(a[ct][i][0] + a[ct][i][1], down, o[ct][2 * b + i][0]);
+            o[ct][2 * b + i][1] = fmaf(a[ct][i][2] + a[ct][i][3], down, o[ct][2 * b + i][1]);
+          }
+      }
     }
+    next_slot();
 
     // ---- end of an item, or of this warp's part
     --todo;
     const bool item_end = cur.ci + 1 == cur.n;
     if (item_end || todo == 0) {
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (g < rows) {
-        const bool whole = item_end && item_head;
-        float* dst;
-        float f = 1.f;
-        if (whole) {
-          dst = out + ((int64_t)cur.s * Hq + head0 + g) * D;
-          f = 1.f / l;
-        } else {
-          // slot 0: the item that the part begins inside of (or holds nothing but); 1: the one it ends inside of
-          float* slot = part + (2ll * wid + (item_head ? 1 : 0)) * paged_part_floats(min(8, G), D);
-          dst = slot + 16 + g * D;
-          if (t == 0) {
-            slot[g] = m;
-            slot[8 + g] = l;
-          }
+      const bool whole = item_end && item_head;
+      // a part in slot 0: the item that the warp's chunks begin inside of (or hold nothing but); 1: the one they end in
+      float* p = part + (2ll * wid + (item_head ? 1 : 0)) * paged_part_floats(min(F::HEADS, G), D);
+#pragma unroll
+      for (int ct = 0; ct < NC; ++ct) {
+        const int h = 4 * ct + t;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
+        if (h >= rows) continue;
+        float* dst = whole ? out + ((int64_t)cur.s * Hq + head0 + h) * D : p + 2 * kMaxTile + h * D;
+        const float f = whole ? 1.f / l[ct] : 1.f;
+        if (!whole && g == 0) {
+          p[h] = m[ct];
+          p[kMaxTile + h] = l[ct];
         }
-        if constexpr (T == kKvF16) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[n][0] * f, o[n][1] * f);
-        } else {
-          // tiles n, n + 1 hold elements 4 t, 4 t + 2 and 4 t + 1, 4 t + 3 of 16
-#pragma unroll
-          for (int n = 0; n < NT; n += 2)
-            *reinterpret_cast<float4*>(dst + 8 * n + 4 * t) =
-                make_float4(o[n][0] * f, o[n + 1][0] * f, o[n][1] * f, o[n + 1][1] * f);
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (T == kKvF16) {
+            dst[16 * n + g] = o[ct][n][0] * f;
+            dst[16 * n + 8 + g] = o[ct][n][1] * f;
+          } else {
+            *reinterpret_cast<float2*>(dst + 16 * n + 2 * g) = make_float2(o[ct][n][0] * f, o[ct][n][1] * f);
+          }
         }
       }
       if (todo == 0) break;
       item_head = true;
       fresh = true;
     }
-    cur.next(c, lens, tiles, CH, status);
+    cur.next(c, lens, rtiles, CH, status);
   }
   cp_async_wait<0>();
   pdl_launch_dependents();
@@ -805,26 +949,32 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D>::CTAS)
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kFewParts = 32;  // one for each lane
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int4* splits, int n_splits,
-                                                                      const float* part, float* __restrict__ out,
-                                                                      int Hq, int n_kv_heads) {
-  extern __shared__ int4 s_item[];  // items of few parts from the front, of many from the back
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int* splits, const int2* split_at,
+                                                                      int n_splits, const float* part,
+                                                                      float* __restrict__ out, int Hq, int G,
+                                                                      int rows) {
+  extern __shared__ int2 s_item[];  // (warp, parts): items of few parts from the front, of many from the back
   __shared__ int s_n[kJoinWarps];
   __shared__ float s_w[kJoinThreads], s_red[kJoinWarps], s_l[kJoinWarps];
   __shared__ __align__(16) float s_o[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = Hq / n_kv_heads, rtiles = (G + 7) >> 3, rows = min(8, G);
   const int64_t stride = paged_part_floats(rows, D);
   int n_few, n_many;
   pdl_wait();
-  {  // the same order in every CTA: thread i takes the i-th run of records
-    const int run = (n_splits + kJoinThreads - 1) / kJoinThreads;
-    const int r0 = min(n_splits, (int)threadIdx.x * run), r1 = min(n_splits, r0 + run);
-    int count = 0;  // few in the low, many in the high half
-    for (int i = r0; i < r1; ++i) {
-      const int parts = splits[i].x;
-      count += parts == 0 ? 0 : parts > kFewParts ? 0x10000 : 1;
+  {  // the same order in every CTA: thread i takes records i, i + kJoinThreads, ...
+    // (up to kRecs of them in registers; a GPU with more warps takes further rounds)
+    constexpr int kRecs = 12;
+    n_few = n_many = 0;
+    for (int base = 0; base < n_splits; base += kRecs * kJoinThreads) {
+    int rec[kRecs];
+#pragma unroll
+    for (int k = 0; k < kRecs; ++k) {
+      const int i = base + k * kJoinThreads + threadIdx.x;
+      rec[k] = i < n_splits ? splits[i] : 0;
     }
+    int count = 0;  // few in the low, many in the high half
+#pragma unroll
+    for (int k = 0; k < kRecs; ++k) count += rec[k] == 0 ? 0 : rec[k] > kFewParts ? 0x10000 : 1;
     int upto = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -839,48 +989,51 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
       if (w < warp) at += s_n[w];
       all += s_n[w];
     }
-    n_few = all & 0xFFFF;
-    n_many = all >> 16;
-    int few = at & 0xFFFF, many = at >> 16;
-    for (int i = r0; i < r1; ++i) {
-      const int4 r = splits[i];
-      if (r.x) s_item[r.x > kFewParts ? n_splits - 1 - many++ : few++] = r;
-    }
+    int few = n_few + (at & 0xFFFF), many = n_many + (at >> 16);
+#pragma unroll
+    for (int k = 0; k < kRecs; ++k)
+      if (rec[k])
+        s_item[rec[k] > kFewParts ? n_splits - 1 - many++ : few++] =
+            make_int2(base + k * kJoinThreads + threadIdx.x, rec[k]);
+    n_few += all & 0xFFFF;
+    n_many += all >> 16;
     __syncthreads();
+    }
   }
-  // part i of an item whose first part is warp w's
-  auto slot = [&](int w, int i) { return part + (2ll * (w + i) + (i == 0 ? 1 : 0)) * stride; };
-  // the query head of row r of an item, -1 behind the last
-  auto head_of = [&](const int4& it, int r) {
-    const int kvh = it.w / rtiles, h = (it.w - kvh * rtiles) * 8 + r;
-    return h < G ? kvh * G + h : -1;
+  // part i of the item that warp w describes: the warp before has the first, in slot 1
+  auto slot = [&](int w, int i) { return part + (2ll * (w - 1 + i) + (i == 0 ? 1 : 0)) * stride; };
+  // the output row of row r of that item, null behind its KV head's last query head
+  auto out_row = [&](int w, int r) -> float* {
+    const int2 at = split_at[w];
+    return at.y % G + r < G ? out + ((int64_t)at.x * Hq + at.y + r) * D : nullptr;
   };
 
   constexpr int COLS = D / 4 < 32 ? D / 4 : 32, GRP = 32 / COLS, V = D / 4 / COLS;  // float4 columns of a row
   for (int u = blockIdx.x * kJoinWarps + warp; u < n_few * rows; u += gridDim.x * kJoinWarps) {
-    const int4 it = s_item[u / rows];
-    const int r = u % rows, h = head_of(it, r);
-    if (h < 0) continue;
+    const int2 it = s_item[u / rows];
+    const int r = u % rows;
+    float* row = out_row(it.x, r);
+    if (!row) continue;
     float w = -INFINITY, l = 0.f;
-    if (lane < it.x) {
-      const float* p = slot(it.y, lane);
+    if (lane < it.y) {
+      const float* p = slot(it.x, lane);
       w = p[r];
-      l = p[8 + r];
+      l = p[kMaxTile + r];
     }
     float M = warp_max(w);
     if (M == -INFINITY) M = 0.f;
-    w = lane < it.x ? ex2(w - M) : 0.f;
+    w = lane < it.y ? ex2(w - M) : 0.f;
     const float f = 1.f / warp_sum(w * l);
     float4 O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     const int grp = lane / COLS, col = lane % COLS;
 #pragma unroll 4
-    for (int i0 = 0; i0 < it.x; i0 += GRP) {
+    for (int i0 = 0; i0 < it.y; i0 += GRP) {
       const int i = i0 + grp;
       const float e = __shfl_sync(0xffffffffu, w, i & 31);
-      if (i < it.x) {
-        const float4* p = reinterpret_cast<const float4*>(slot(it.y, i) + 16 + r * D) + col;
+      if (i < it.y) {
+        const float4* p = reinterpret_cast<const float4*>(slot(it.x, i) + 2 * kMaxTile + r * D) + col;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float4 x = p[v * COLS];
@@ -897,7 +1050,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
       O[0].z += __shfl_xor_sync(0xffffffffu, O[0].z, 16);
       O[0].w += __shfl_xor_sync(0xffffffffu, O[0].w, 16);
     }
-    float4* dst = reinterpret_cast<float4*>(out + ((int64_t)it.z * Hq + h) * D) + col;
+    float4* dst = reinterpret_cast<float4*>(row) + col;
     if (grp == 0)
 #pragma unroll
       for (int v = 0; v < V; ++v) dst[v * COLS] = make_float4(O[v].x * f, O[v].y * f, O[v].z * f, O[v].w * f);
@@ -905,11 +1058,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
 
   constexpr int Z = D / 32;
   for (int u = blockIdx.x; u < n_many * rows * Z; u += gridDim.x) {
-    const int4 it = s_item[n_splits - 1 - u / (rows * Z)];
-    const int r = u / Z % rows, z = u % Z, h = head_of(it, r);
-    if (h < 0) continue;
+    const int2 it = s_item[n_splits - 1 - u / (rows * Z)];
+    const int r = u / Z % rows, z = u % Z;
+    float* row = out_row(it.x, r);
+    if (!row) continue;
     float M = -INFINITY;
-    for (int i = threadIdx.x; i < it.x; i += kJoinThreads) M = fmaxf(M, slot(it.y, i)[r]);
+    for (int i = threadIdx.x; i < it.y; i += kJoinThreads) M = fmaxf(M, slot(it.x, i)[r]);
     M = warp_max(M);
     __syncthreads();  // the last item's reads of the shared arrays are done
     if (lane == 0) s_red[warp] = M;
@@ -921,20 +1075,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     const int sub = threadIdx.x >> 3, e = (threadIdx.x & 7) * 4;  // 8 threads read the 32 elements of a part
-    for (int base = 0; base < it.x; base += kJoinThreads) {
-      const int cnt = min(kJoinThreads, it.x - base);
+    for (int base = 0; base < it.y; base += kJoinThreads) {
+      const int cnt = min(kJoinThreads, it.y - base);
       if (base) __syncthreads();
       if ((int)threadIdx.x < cnt) {
-        const float* p = slot(it.y, base + threadIdx.x);
+        const float* p = slot(it.x, base + threadIdx.x);
         const float f = ex2(p[r] - M);
         s_w[threadIdx.x] = f;
-        L = fmaf(p[8 + r], f, L);
+        L = fmaf(p[kMaxTile + r], f, L);
       }
       __syncthreads();
 #pragma unroll 4
       for (int i = sub; i < cnt; i += kJoinThreads / 8) {
         const float f = s_w[i];
-        const float4 v = *reinterpret_cast<const float4*>(slot(it.y, base + i) + 16 + r * D + 32 * z + e);
+        const float4 v = *reinterpret_cast<const float4*>(slot(it.x, base + i) + 2 * kMaxTile + r * D + 32 * z + e);
         O.x = fmaf(v.x, f, O.x);
         O.y = fmaf(v.y, f, O.y);
         O.z = fmaf(v.z, f, O.z);
@@ -959,7 +1113,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
         sum += s_o[i][lane];
         tot += s_l[i];
       }
-      out[((int64_t)it.z * Hq + h) * D + 32 * z + lane] = sum / tot;
+      row[32 * z + lane] = sum / tot;
     }
   }
 }

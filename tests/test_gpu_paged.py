@@ -7,18 +7,21 @@ squares is off by at most log2-depth-plus-lane-steps 2^-24 (<= 16 of them, half
 of that through the root), division, root, two products, then cos and sin
 rounded to fp32 and three operations, at most 20 half-steps of 2^-24 in all
 (1.2e-6).  Attention: with e = 2^-23,
-  |diff| <= (2 ds + (n/16 + 64) e) sum_p p_p |v_p| + n 2^-38 max|v|,
+  |diff| <= (2 ds + (n/16 + 64) e) sum_p p_p |v_p| + (n 2^-35 + 2^-29) max|v|,
   ds = (D + 8) e max_p (scale sum_i |q_i k_i|) + 4 e max_p |s_p|
 (ds: a score's error with every one of its D products and sums off by a step,
 and the scaling and the exponential's argument; a probability moves by at most
 2 ds relative, numerator and sum together; the weighted sums take at most one
-rounding for every 16 positions and 64 for the joins).  The last term: p times
-the values' scale enters the products as a sum of two fp16 numbers after a power
-of two that puts the chunk's largest possible product in [2^13, 2^14].  The
-second number is rounded to the nearest multiple of 2^-24 where it is subnormal,
-an error of at most 2^-25 whatever p, i.e. 2^-25 / 2^13 = 2^-38 of the largest
-scale, times the code: at most 2^-38 max|v| for each of the n positions, however
-small its p.  (Where one position takes all and its value is zero, that is all
+rounding for every 16 positions and 64 for the joins).  The last term: p enters the
+products 2^10 fold as a sum of two fp16 numbers (2^14 fold for F16); the second
+is rounded to the nearest multiple of 2^-24 where it is subnormal, an error of
+at most 2^-25 whatever p, 2^-35 of the largest weight, for each of the n
+positions.  A value block's scale enters times a power of two that puts the
+chunk's largest at 2^4 or more, rounded to a multiple of 2^-24 below 2^-14: at
+most 2^-25 / 2^4 = 2^-29 of the largest, weighted with p, whose sum is 1.  Where
+all scales are subnormal (below 2^-14) p is scaled by up to 2^14 and the largest
+product is at least 2^5: 2^-25 / 2^5 = 2^-30 instead of 2^-35.
+(Where one position takes all and its value is zero, that is all
 there is: without the term, 4-bit values of exactly zero would demand an output
 right to 2^-15 of a weight of 1e-10.)"""
 import numpy as np
@@ -141,6 +144,8 @@ def attention_ref(cache, q, lens, hq, scale):
         if n == 0:
             continue
         k, v = cache.seq_values(0, s, n), cache.seq_values(1, s, n)
+        top_scale = np.abs(v).max() / {F16: 1e-9, Q8: 127, Q4: 8}[cache.kind]
+        tiny = 2.0 ** (-30 if top_scale < 2.0 ** -14 else -35)
         for h in range(hq):
             a = q[s, h].astype(np.float64)
             x = scale * (k[h // g] @ a)
@@ -149,7 +154,7 @@ def attention_ref(cache, q, lens, hq, scale):
             out[s, h] = p @ v[h // g]
             ds = (cache.d + 8) * STEP * abs(scale) * (np.abs(k[h // g]) @ np.abs(a)).max() + 4 * STEP * np.abs(x).max()
             bound[s, h] = (2 * ds + (n / 16 + 64) * STEP) * (p @ np.abs(v[h // g])) \
-                + n * 2.0 ** -38 * np.abs(v[h // g]).max()
+                + (n * tiny + 2.0 ** -29) * np.abs(v[h // g]).max()
     return out, bound
 
 
