@@ -13,7 +13,6 @@
 namespace ntx {
 namespace {
 
-constexpr int kMaxPagedSeqs = 1024;
 constexpr int kMaxGroup = 64;
 
 int failf(int code, const char* fmt, ...) {
@@ -139,14 +138,14 @@ cudaError_t with_attn(const ntx_paged_kv* kv, int n_q_heads, F f) {
   });
 }
 
-// Workspace: a record of 16 bytes for each warp of the attention kernel, then two parts for each.
+// Workspace: two parts for each warp of the attention kernel.
 size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
   size_t n = 0;
   with_attn(kv, n_q_heads, [&](auto t, auto d, auto nc) {
     using F = PagedCfg<decltype(t)::value, decltype(d)::value, decltype(nc)::value>;
     const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
     const int G = n_q_heads / kv->n_kv_heads;
-    n = warps * (16 + 2 * sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
+    n = warps * (2 * sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
     return cudaSuccess;
   });
   return n;
@@ -156,30 +155,25 @@ template <int T, int D, int NC>
 cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
                               const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
   using F = PagedCfg<T, D, NC>;
-  static std::atomic<unsigned long long> done{0}, done_join{0};
-  const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS, G = Hq / kv.n_kv_heads;
-  // records of 4 and 8 bytes, then the parts, 16-byte aligned
-  int* splits = static_cast<int*>(ws);
-  int2* split_at = reinterpret_cast<int2*>(splits + warps);
-  float* part = reinterpret_cast<float*>(splits + 4 * (size_t)warps);
+  static std::atomic<unsigned long long> done{0};
+  const int grid = sm_count() * F::CTAS;
+  float* part = static_cast<float*>(ws);
+  int* status = device_status_ptr();
   cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC>, F::SMEM, done);
-  if (e == cudaSuccess) e = allow_smem(attn_paged_join_kernel<D>, 64 * 1024, done_join);
   if (e != cudaSuccess) return e;
-  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, splits, split_at, part, Hq, lens,
-                                                                   scale, device_status_ptr());
+  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, part, Hq, lens, scale, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count() * 4);
+  cfg.gridDim = dim3(sm_count() * 8);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = warps * sizeof(int2);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int*)splits, (const int2*)split_at, warps,
-                            (const float*)part, out, Hq, G, G < F::HEADS ? G : F::HEADS);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, kv, (const float*)part, out, Hq, lens, (int)F::CH,
+                            (int)F::HEADS, grid * F::WARPS, status);
 }
 
 int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }

@@ -345,7 +345,7 @@ template <int T, int D, int NC>
 struct PagedCfg {
   static constexpr int CH = (T == kKvF16 && D == 256) ? 16 : 32;
   static constexpr int SLOTS = (T == kKvF16 || (T == kKvQ8 && D >= 128)) ? 3 : 4;
-  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 128 ? 4 : D * NC <= 256 ? 3 : 2;
+  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : D * NC <= 256 ? 3 : 2;
   static constexpr int HEADS = 4 * NC;                     // query heads of a tile
   static constexpr int WARPS = 4;
   static constexpr int CB = kv_code_bytes<T>(D);           // bytes of a row's codes
@@ -382,59 +382,65 @@ __device__ __forceinline__ int seq_len(const ntx_paged_kv& c, const int* lens, i
 // `kvh` of sequence `s`.
 struct PagedCursor {
   int s, kvh, rt, ci, n, len;
-  // to the next chunk; true where it is the first of an item
-  __device__ __forceinline__ bool next(const ntx_paged_kv& c, const int* lens, int rtiles, int ch, int* status) {
-    if (++ci < n) return false;
+  __device__ __forceinline__ void next(const ntx_paged_kv& c, const int* lens, int rtiles, int ch, int* status) {
+    if (++ci < n) return;
     ci = 0;
-    if (++rt < rtiles) return true;
+    if (++rt < rtiles) return;
     rt = 0;
-    if (++kvh < c.n_kv_heads) return true;
+    if (++kvh < c.n_kv_heads) return;
     kvh = 0;
     do {
-      if (++s >= c.n_seqs) { n = 0; return true; }
+      if (++s >= c.n_seqs) { n = 0; return; }
       len = seq_len(c, lens, s, status);
       n = (len + ch - 1) / ch;
     } while (n == 0);
-    return true;
   }
 };
 
-// W chunks in consecutive parts for at most `warps` warps, sizes differing by one at most.
+// Work is counted in units: each chunk one, and kItemUnits more for the start of
+// each item (q's fragments, an output to write).  W units in consecutive parts for
+// at most `warps` warps, sizes differing by one at most.
+constexpr int kItemUnits = 1;
 struct PagedParts {
   int n;
-  int64_t size, longer;  // the first `longer` parts have size + 1 chunks
+  int64_t size, longer;  // the first `longer` parts have size + 1 units
   __device__ __forceinline__ PagedParts(int64_t W, int warps) : n((int)min64(W, warps)), size(0), longer(0) {
     if (n == 0) return;
     size = W >> 31 ? W / n : (int)W / n;
     longer = W - size * n;
   }
   __device__ __forceinline__ int64_t begin(int w) const { return w * size + min64(w, longer); }
-  __device__ __forceinline__ int holder(int64_t chunk) const {
+  __device__ __forceinline__ int holder(int64_t unit) const {  // the part of a unit
     const int64_t head = longer * (size + 1);
-    if (chunk < head) return (int)(chunk >> 31 ? chunk / (size + 1) : (int)chunk / (int)(size + 1));
-    chunk -= head;
-    return (int)(longer + (chunk >> 31 ? chunk / size : (int)chunk / (int)size));
+    if (unit < head) return (int)(unit >> 31 ? unit / (size + 1) : (int)unit / (int)(size + 1));
+    unit -= head;
+    return (int)(longer + (unit >> 31 ? unit / size : (int)unit / (int)size));
   }
 };
+// Units of each of a sequence's items.
+__device__ __forceinline__ int item_units(int chunks) { return chunks ? chunks + kItemUnits : 0; }
 
-// Chunks of all sequences before `upto` (all of them: upto >= n_seqs), one tile each.
-// Lane i counts k consecutive sequences.
-__device__ __forceinline__ int64_t lane_chunks(const ntx_paged_kv& c, const int* lens, int k, int ch, int upto,
-                                               int* status) {
+// Units of the items of k consecutive sequences to a lane (`mine`) and of all up to and with them.
+__device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* lens, int k, int ch, int tiles,
+                                              int64_t& mine, int* status) {
   const int lane = threadIdx.x & 31;
-  int64_t sum = 0;
-  for (int i = 0; i < k; ++i) {
-    const int s = lane * k + i;
-    if (s < c.n_seqs && s < upto) sum += (seq_len(c, lens, s, status) + ch - 1) / ch;
+  mine = 0;
+  for (int i = 0; i < k; ++i)
+    if (lane * k + i < c.n_seqs) mine += item_units((seq_len(c, lens, lane * k + i, status) + ch - 1) / ch);
+  mine *= tiles;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-  return sum;
+  return upto;
 }
 
 template <int T, int D, int NC>
 __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     attn_paged_kernel(const ntx_paged_kv c, const float* __restrict__ q, int64_t qs, float* __restrict__ out,
-                      int* __restrict__ splits, int2* __restrict__ split_at, float* __restrict__ part, int Hq,
-                      const int* __restrict__ lens, float scale, int* status) {
+                      float* __restrict__ part, int Hq, const int* __restrict__ lens, float scale, int* status) {
   using F = PagedCfg<T, D, NC>;
   constexpr int CH = F::CH, C = F::CB / 16, NB = D / 32, NS = CH / 16, NT = D / 16;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -442,7 +448,8 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
   const uint32_t slots = smem_addr(ring) + warp * (F::SLOTS * F::SLOT);
   const int G = Hq / c.n_kv_heads, rtiles = (G + F::HEADS - 1) / F::HEADS;
   const int tiles = c.n_kv_heads * rtiles;
-  const int wid = warp * gridDim.x + blockIdx.x, all_warps = gridDim.x * F::WARPS;
+  const int wid = blockIdx.x * F::WARPS + warp, all_warps = gridDim.x * F::WARPS;
+  pdl_launch_dependents();  // the join's CTAs prepare themselves where there is room
 
   // empty sequences: zeros
   for (int s = wid; s < c.n_seqs; s += all_warps)
@@ -450,52 +457,38 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
       for (int64_t i = lane; i < (int64_t)Hq * D / 4; i += 32)
         reinterpret_cast<float4*>(out + (int64_t)s * Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  // ---- this warp's part of the chunks, [c0, c1)
+  // ---- this warp's part: its first chunk, and `todo` units from there
   PagedCursor cur;
   int64_t todo;
-  bool item_head;  // false: the part begins inside an item
   {
-    const int k = (c.n_seqs + 31) >> 5;
-    const int64_t mine = lane_chunks(c, lens, k, CH, c.n_seqs, status) * tiles;
-    int64_t upto = mine;  // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const int64_t W = __shfl_sync(0xffffffffu, upto, 31);
-    const PagedParts parts_of(W, all_warps);
-    if (wid >= parts_of.n) {
-      if (lane == 0) splits[wid] = 0;
-      return;
-    }
-    const int64_t c0 = parts_of.begin(wid);
-    todo = parts_of.begin(wid + 1) - c0;
-    const int at = __ffs(__ballot_sync(0xffffffffu, upto > c0)) - 1;  // the lane whose sequences hold c0
-    int64_t rest = c0 - __shfl_sync(0xffffffffu, upto - mine, at);
+    const int k = (c.n_seqs + 31) >> 5;  // sequences to a lane
+    int64_t mine;
+    const int64_t upto = lane_units(c, lens, k, CH, tiles, mine, status);
+    const PagedParts parts(__shfl_sync(0xffffffffu, upto, 31), all_warps);
+    if (wid >= parts.n) return;
+    const int64_t u0 = parts.begin(wid);
+    todo = parts.begin(wid + 1) - u0;
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1;  // the lane whose sequences hold u0
+    int64_t rest = u0 - __shfl_sync(0xffffffffu, upto - mine, at);
     cur.s = at * k;
+    int units;
     for (;;) {
       cur.len = seq_len(c, lens, cur.s, status);
       cur.n = (cur.len + CH - 1) / CH;
-      if (rest < (int64_t)cur.n * tiles) break;
-      rest -= (int64_t)cur.n * tiles;
+      units = item_units(cur.n);
+      if (rest < (int64_t)units * tiles) break;
+      rest -= (int64_t)units * tiles;
       ++cur.s;
     }
-    const int tile = (int)(rest / cur.n);
-    cur.ci = (int)(rest - (int64_t)tile * cur.n);
+    const int tile = (int)(rest >> 31 ? rest / units : (int)rest / units);
+    const int in_item = (int)(rest - (int64_t)tile * units);
+    cur.ci = max(0, in_item - kItemUnits);
     cur.kvh = tile / rtiles;
     cur.rt = tile - cur.kvh * rtiles;
-    item_head = cur.ci == 0;
-    // The first warp that begins inside an item describes it for the join: its
-    // parts lie in slot 1 of the warp before and slot 0 of this and the next ones.
-    if (lane == 0) {
-      const int64_t first = c0 - cur.ci;
-      int parts = 0;
-      if (!item_head && parts_of.begin(wid - 1) <= first) parts = parts_of.holder(first + cur.n - 1) - wid + 2;
-      splits[wid] = parts;
-      split_at[wid] = make_int2(cur.s, cur.kvh * G + F::HEADS * cur.rt);
-    }
+    todo -= max(0, kItemUnits - in_item);
+    if (todo <= 0) return;
   }
+  bool item_head = cur.ci == 0;  // false: the part begins inside an item
 
   // ---- loading: the ring's next slot takes K or V of chunk `ld`, 16 rows (one page) at a time
   const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D), scales_at = (int64_t)c.page_size * F::CB;
@@ -507,6 +500,10 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     if (item) {
       ld_j = ld.ci * CH / c.page_size;
       ld_row = ld.ci * CH - ld_j * c.page_size;
+      const int h0 = F::HEADS * ld.rt;  // its query heads are read a chunk from now
+      const float* qp = q + ld.s * qs + (int64_t)(ld.kvh * G + h0) * D;
+      for (int i = lane; i < min(F::HEADS, G - h0) * (D / 32); i += 32)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(qp + 32 * i));
     }
     const int* row = c.page_table + (int64_t)ld.s * c.max_pages;
 #pragma unroll
@@ -570,7 +567,14 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
       ld_slot = ld_slot + F::SLOT == slots + F::SLOTS * F::SLOT ? slots : ld_slot + F::SLOT;
       if constexpr (V) {
         // the pages of the next chunk are used half a chunk from now
-        if (--ld_left > 0) look_up(ld.next(c, lens, rtiles, CH, status));
+        if (--ld_left > 0) {
+          const bool item = ld.ci + 1 == ld.n;
+          if (item) ld_left -= kItemUnits;
+          if (ld_left > 0) {
+            ld.next(c, lens, rtiles, CH, status);
+            look_up(item);
+          }
+        }
       }
     }
     cp_async_commit();
@@ -906,9 +910,10 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     // ---- end of an item, or of this warp's part
     --todo;
     const bool item_end = cur.ci + 1 == cur.n;
-    if (item_end || todo == 0) {
+    if (item_end) todo -= kItemUnits;
+    if (item_end || todo <= 0) {
       const bool whole = item_end && item_head;
-      // a part in slot 0: the item that the warp's chunks begin inside of (or hold nothing but); 1: the one they end in
+      // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
       float* p = part + (2ll * wid + (item_head ? 1 : 0)) * paged_part_floats(min(F::HEADS, G), D);
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
@@ -932,190 +937,186 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
           }
         }
       }
-      if (todo == 0) break;
+      if (todo <= 0) break;
       item_head = true;
       fresh = true;
     }
     cur.next(c, lens, rtiles, CH, status);
   }
   cp_async_wait<0>();
-  pdl_launch_dependents();
 }
 
 // Joins the parts of the items that several warps hold: with M the largest m,
-// out = sum 2^(m - M) o / sum 2^(m - M) l.  Every CTA gathers the split items
-// (main kernel's records, in shared memory); then each warp takes (item, head)
-// pairs of few parts, and each CTA (item, head, 32 elements) of many.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kFewParts = 32;  // one for each lane
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int* splits, const int2* split_at,
-                                                                      int n_splits, const float* part,
-                                                                      float* __restrict__ out, int Hq, int G,
-                                                                      int rows) {
-  extern __shared__ int2 s_item[];  // (warp, parts): items of few parts from the front, of many from the back
-  __shared__ int s_n[kJoinWarps];
-  __shared__ float s_w[kJoinThreads], s_red[kJoinWarps], s_l[kJoinWarps];
-  __shared__ __align__(16) float s_o[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t stride = paged_part_floats(rows, D);
-  int n_few, n_many;
-  pdl_wait();
-  {  // the same order in every CTA: thread i takes records i, i + kJoinThreads, ...
-    // (up to kRecs of them in registers; a GPU with more warps takes further rounds)
-    constexpr int kRecs = 12;
-    n_few = n_many = 0;
-    for (int base = 0; base < n_splits; base += kRecs * kJoinThreads) {
-    int rec[kRecs];
-#pragma unroll
-    for (int k = 0; k < kRecs; ++k) {
-      const int i = base + k * kJoinThreads + threadIdx.x;
-      rec[k] = i < n_splits ? splits[i] : 0;
-    }
-    int count = 0;  // few in the low, many in the high half
-#pragma unroll
-    for (int k = 0; k < kRecs; ++k) count += rec[k] == 0 ? 0 : rec[k] > kFewParts ? 0x10000 : 1;
-    int upto = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) s_n[warp] = upto;
-    __syncthreads();
-    int at = upto - count, all = 0;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) at += s_n[w];
-      all += s_n[w];
-    }
-    int few = n_few + (at & 0xFFFF), many = n_many + (at >> 16);
-#pragma unroll
-    for (int k = 0; k < kRecs; ++k)
-      if (rec[k])
-        s_item[rec[k] > kFewParts ? n_splits - 1 - many++ : few++] =
-            make_int2(base + k * kJoinThreads + threadIdx.x, rec[k]);
-    n_few += all & 0xFFFF;
-    n_many += all >> 16;
-    __syncthreads();
-    }
-  }
-  // part i of the item that warp w describes: the warp before has the first, in slot 1
-  auto slot = [&](int w, int i) { return part + (2ll * (w - 1 + i) + (i == 0 ? 1 : 0)) * stride; };
-  // the output row of row r of that item, null behind its KV head's last query head
-  auto out_row = [&](int w, int r) -> float* {
-    const int2 at = split_at[w];
-    return at.y % G + r < G ? out + ((int64_t)at.x * Hq + at.y + r) * D : nullptr;
-  };
+// out = sum 2^(m - M) o / sum 2^(m - M) l.  Which warps those are follows from the
+// lengths alone (read before the main kernel's end: no kernel of the call writes
+// them).  A warp takes 32 elements of an (item, head), four parts at a time; for
+// sequences of many parts a CTA does, 32 at a time.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr int kFewParts = 28;
+constexpr int kMaxPagedSeqs = 1024;
 
-  constexpr int COLS = D / 4 < 32 ? D / 4 : 32, GRP = 32 / COLS, V = D / 4 / COLS;  // float4 columns of a row
-  for (int u = blockIdx.x * kJoinWarps + warp; u < n_few * rows; u += gridDim.x * kJoinWarps) {
-    const int2 it = s_item[u / rows];
-    const int r = u % rows;
-    float* row = out_row(it.x, r);
-    if (!row) continue;
-    float w = -INFINITY, l = 0.f;
-    if (lane < it.y) {
-      const float* p = slot(it.x, lane);
-      w = p[r];
-      l = p[kMaxTile + r];
-    }
-    float M = warp_max(w);
-    if (M == -INFINITY) M = 0.f;
-    w = lane < it.y ? ex2(w - M) : 0.f;
-    const float f = 1.f / warp_sum(w * l);
-    float4 O[V];
+struct PagedMerge {  // a running join of parts, four elements a thread
+  float M = -INFINITY, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void scale_to(float m) {
+    const float f = ex2(M - (m == -INFINITY ? 0.f : m));
+    M = m;
+    L *= f;
+    O.x *= f; O.y *= f; O.z *= f; O.w *= f;
+  }
+  __device__ __forceinline__ void add(float m, float l, float4 o) {  // M is at least m
+    const float f = ex2(m - (M == -INFINITY ? 0.f : M));
+    L = fmaf(l, f, L);
+    O.x = fmaf(o.x, f, O.x); O.y = fmaf(o.y, f, O.y); O.z = fmaf(o.z, f, O.z); O.w = fmaf(o.w, f, O.w);
+  }
+  // parts first, first + step, ... below n; at(i) is part i, `row` and `e` the head and the element in it
+  template <int BATCH, class At>
+  __device__ __forceinline__ void parts(At at, int first, int step, int n, int row, int e) {
+    for (int i0 = first; i0 < n; i0 += step * BATCH) {
+      float m[BATCH], l[BATCH], top = M;
+      float4 o[BATCH];
 #pragma unroll
-    for (int v = 0; v < V; ++v) O[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int grp = lane / COLS, col = lane % COLS;
-#pragma unroll 4
-    for (int i0 = 0; i0 < it.y; i0 += GRP) {
-      const int i = i0 + grp;
-      const float e = __shfl_sync(0xffffffffu, w, i & 31);
-      if (i < it.y) {
-        const float4* p = reinterpret_cast<const float4*>(slot(it.x, i) + 2 * kMaxTile + r * D) + col;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float4 x = p[v * COLS];
-          O[v].x = fmaf(x.x, e, O[v].x);
-          O[v].y = fmaf(x.y, e, O[v].y);
-          O[v].z = fmaf(x.z, e, O[v].z);
-          O[v].w = fmaf(x.w, e, O[v].w);
+      for (int b = 0; b < BATCH; ++b) {
+        const int i = i0 + b * step;
+        const float* p = at(min(i, n - 1));
+        m[b] = i < n ? p[row] : -INFINITY;
+        l[b] = p[kMaxTile + row];
+        o[b] = *reinterpret_cast<const float4*>(p + e);
+        if (i >= n) {
+          l[b] = 0.f;
+          o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
-    }
-    if constexpr (GRP == 2) {
-      O[0].x += __shfl_xor_sync(0xffffffffu, O[0].x, 16);
-      O[0].y += __shfl_xor_sync(0xffffffffu, O[0].y, 16);
-      O[0].z += __shfl_xor_sync(0xffffffffu, O[0].z, 16);
-      O[0].w += __shfl_xor_sync(0xffffffffu, O[0].w, 16);
-    }
-    float4* dst = reinterpret_cast<float4*>(row) + col;
-    if (grp == 0)
 #pragma unroll
-      for (int v = 0; v < V; ++v) dst[v * COLS] = make_float4(O[v].x * f, O[v].y * f, O[v].z * f, O[v].w * f);
+      for (int b = 0; b < BATCH; ++b) top = fmaxf(top, m[b]);
+      scale_to(top);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) add(m[b], l[b], o[b]);
+    }
   }
+  __device__ __forceinline__ void with_lane(int x) {  // and the parts of the lane `x` away
+    scale_to(fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x)));
+    L += __shfl_xor_sync(0xffffffffu, L, x);
+    O.x += __shfl_xor_sync(0xffffffffu, O.x, x);
+    O.y += __shfl_xor_sync(0xffffffffu, O.y, x);
+    O.z += __shfl_xor_sync(0xffffffffu, O.z, x);
+    O.w += __shfl_xor_sync(0xffffffffu, O.w, x);
+  }
+};
 
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const ntx_paged_kv c, const float* part,
+                                                                      float* __restrict__ out, int Hq,
+                                                                      const int* __restrict__ lens, int ch,
+                                                                      int tile_heads, int all_warps, int* status) {
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ __align__(16) float s_o[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = Hq / c.n_kv_heads, rtiles = (G + tile_heads - 1) / tile_heads, tiles = c.n_kv_heads * rtiles;
+  const int rows = min(tile_heads, G);
+  const int64_t stride = paged_part_floats(rows, D);
+  const int k = (c.n_seqs + 31) >> 5;  // sequences to a lane
+  int64_t mine;
+  const int64_t upto = lane_units(c, lens, k, ch, tiles, mine, status);
+  const PagedParts parts(__shfl_sync(0xffffffffu, upto, 31), all_warps);
+  auto chunks = [&](int s) { return (seq_len(c, lens, s, status) + ch - 1) / ch; };
+  auto many = [&](int n) { return n > kFewParts * parts.size; };
+
+  // (item, head, 32 elements) j of a sequence of n chunks: the parts' first warp and number, and the output
+  struct Unit {
+    int w0, cnt, r;
+    float* row;
+  };
   constexpr int Z = D / 32;
-  for (int u = blockIdx.x; u < n_many * rows * Z; u += gridDim.x) {
-    const int2 it = s_item[n_splits - 1 - u / (rows * Z)];
-    const int r = u / Z % rows, z = u % Z;
-    float* row = out_row(it.x, r);
-    if (!row) continue;
-    float M = -INFINITY;
-    for (int i = threadIdx.x; i < it.y; i += kJoinThreads) M = fmaxf(M, slot(it.x, i)[r]);
-    M = warp_max(M);
-    __syncthreads();  // the last item's reads of the shared arrays are done
-    if (lane == 0) s_red[warp] = M;
-    __syncthreads();
-    M = s_red[0];
-#pragma unroll
-    for (int i = 1; i < kJoinWarps; ++i) M = fmaxf(M, s_red[i]);
-    if (M == -INFINITY) M = 0.f;
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int sub = threadIdx.x >> 3, e = (threadIdx.x & 7) * 4;  // 8 threads read the 32 elements of a part
-    for (int base = 0; base < it.y; base += kJoinThreads) {
-      const int cnt = min(kJoinThreads, it.y - base);
-      if (base) __syncthreads();
-      if ((int)threadIdx.x < cnt) {
-        const float* p = slot(it.x, base + threadIdx.x);
-        const float f = ex2(p[r] - M);
-        s_w[threadIdx.x] = f;
-        L = fmaf(p[kMaxTile + r], f, L);
+  const int per_seq = tiles * rows * Z;
+  auto unit = [&](int s, int n, int j) {
+    Unit u;
+    const int z = j % Z, tile = j / Z / rows;
+    u.r = j / Z - tile * rows;
+    const int kvh = tile / rtiles, h = (tile - kvh * rtiles) * tile_heads + u.r;
+    u.row = h < G ? out + ((int64_t)s * Hq + kvh * G + h) * D + 32 * z : nullptr;
+    const int holder = s / k;
+    int64_t first = __shfl_sync(0xffffffffu, upto - mine, holder);
+    for (int i = holder * k; i < s; ++i) first += (int64_t)item_units(chunks(i)) * tiles;
+    first += (int64_t)tile * item_units(n) + kItemUnits;
+    u.w0 = parts.holder(first);
+    u.cnt = parts.holder(first + n - 1) - u.w0 + 1;
+    return u;
+  };
+  // part i of an item: the first is in its warp's slot 1
+  auto part_of = [&](const Unit& u, int i) { return part + (2ll * (u.w0 + i) + (i == 0 ? 1 : 0)) * stride; };
+  bool waited = false;
+  auto wait = [&]() {
+    if (!waited) pdl_wait();
+    waited = true;
+  };
+
+  // the sequences of many parts: bit `lane` for each of the lane's sequences in turn
+  int n_many = 0;
+  for (int i = 0; i < k; ++i) {
+    const int s = lane * k + i;
+    n_many += __popc(__ballot_sync(0xffffffffu, s < c.n_seqs && many(chunks(s))));
+  }
+  for (int64_t x = blockIdx.x; x < (int64_t)n_many * per_seq; x += gridDim.x) {
+    int nth = (int)(x / per_seq), s = 0;
+    for (int i = 0; i < k; ++i) {
+      const int cand = lane * k + i;
+      unsigned mask = __ballot_sync(0xffffffffu, cand < c.n_seqs && many(chunks(cand)));
+      if (nth < __popc(mask)) {
+        for (; nth > 0; --nth) mask &= mask - 1;
+        s = (__ffs(mask) - 1) * k + i;
+        break;
       }
-      __syncthreads();
-#pragma unroll 4
-      for (int i = sub; i < cnt; i += kJoinThreads / 8) {
-        const float f = s_w[i];
-        const float4 v = *reinterpret_cast<const float4*>(slot(it.x, base + i) + 2 * kMaxTile + r * D + 32 * z + e);
-        O.x = fmaf(v.x, f, O.x);
-        O.y = fmaf(v.y, f, O.y);
-        O.z = fmaf(v.z, f, O.z);
-        O.w = fmaf(v.w, f, O.w);
-      }
+      nth -= __popc(mask);
     }
-    L = warp_sum(L);
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
-      O.x += __shfl_xor_sync(0xffffffffu, O.x, o);
-      O.y += __shfl_xor_sync(0xffffffffu, O.y, o);
-      O.z += __shfl_xor_sync(0xffffffffu, O.z, o);
-      O.w += __shfl_xor_sync(0xffffffffu, O.w, o);
+    const int j = (int)(x % per_seq);
+    const Unit u = unit(s, chunks(s), j);
+    if (!u.row) continue;
+    wait();
+    PagedMerge y;  // eight threads read the 32 elements of a part
+    y.parts<4>([&](int i) { return part_of(u, i); }, threadIdx.x >> 3, kJoinThreads / 8, u.cnt, u.r,
+               2 * kMaxTile + u.r * D + j % Z * 32 + lane % 8 * 4);
+    y.with_lane(8);
+    y.with_lane(16);
+    __syncthreads();  // the last unit's reads are done
+    if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = y.O;
+    if (lane == 0) {
+      s_m[warp] = y.M;
+      s_l[warp] = y.L;
     }
-    if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][e]) = O;
-    if (lane == 0) s_l[warp] = L;
     __syncthreads();
     if (warp == 0) {
-      float sum = 0.f, tot = 0.f;
+      float M = s_m[0], sum = 0.f, tot = 0.f;
+#pragma unroll
+      for (int i = 1; i < kJoinWarps; ++i) M = fmaxf(M, s_m[i]);
+      if (M == -INFINITY) M = 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinWarps; ++i) {
-        sum += s_o[i][lane];
-        tot += s_l[i];
+        const float f = ex2(s_m[i] - M);
+        sum = fmaf(s_o[i][lane], f, sum);
+        tot = fmaf(s_l[i], f, tot);
       }
-      row[32 * z + lane] = sum / tot;
+      u.row[lane] = sum / tot;
     }
   }
+
+  for (int64_t x = (int64_t)blockIdx.x * kJoinWarps + warp; x < (int64_t)c.n_seqs * per_seq;
+       x += (int64_t)gridDim.x * kJoinWarps) {
+    const int s = (int)(x >> 31 ? x / per_seq : (int)x / per_seq), j = (int)(x - (int64_t)s * per_seq), n = chunks(s);
+    if (n == 0 || many(n)) continue;
+    const Unit u = unit(s, n, j);
+    if (u.cnt < 2 || !u.row) continue;
+    wait();
+    PagedMerge y;
+    y.parts<4>([&](int i) { return part_of(u, i); }, lane >> 3, 4, u.cnt, u.r,
+               2 * kMaxTile + u.r * D + j % Z * 32 + lane % 8 * 4);
+    y.with_lane(8);
+    y.with_lane(16);
+    const float f = 1.f / y.L;
+    if (lane < 8)
+      *reinterpret_cast<float4*>(u.row + lane * 4) = make_float4(y.O.x * f, y.O.y * f, y.O.z * f, y.O.w * f);
+  }
+  wait();  // completion of this kernel implies the main kernel's
 }
 
 }  // namespace ntx
