@@ -138,14 +138,14 @@ cudaError_t with_attn(const ntx_paged_kv* kv, int n_q_heads, F f) {
   });
 }
 
-// Workspace: two parts for each warp of the attention kernel.
+// Workspace: two records of 16 bytes and two parts for each warp of the attention kernel.
 size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
   size_t n = 0;
   with_attn(kv, n_q_heads, [&](auto t, auto d, auto nc) {
     using F = PagedCfg<decltype(t)::value, decltype(d)::value, decltype(nc)::value>;
     const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
     const int G = n_q_heads / kv->n_kv_heads;
-    n = warps * (2 * sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
+    n = warps * 2 * (sizeof(int4) + sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
     return cudaSuccess;
   });
   return n;
@@ -156,15 +156,16 @@ cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs
                               const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
   using F = PagedCfg<T, D, NC>;
   static std::atomic<unsigned long long> done{0};
-  const int grid = sm_count() * F::CTAS;
-  float* part = static_cast<float*>(ws);
-  int* status = device_status_ptr();
+  const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS, G = Hq / kv.n_kv_heads;
+  int4* split = static_cast<int4*>(ws);
+  float* part = reinterpret_cast<float*>(split + 2 * (size_t)warps);
   cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC>, F::SMEM, done);
   if (e != cudaSuccess) return e;
-  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, part, Hq, lens, scale, status);
+  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, split, part, Hq, lens, scale,
+                                                                       device_status_ptr());
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count() * 8);
+  cfg.gridDim = dim3(warps);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -172,8 +173,8 @@ cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, kv, (const float*)part, out, Hq, lens, (int)F::CH,
-                            (int)F::HEADS, grid * F::WARPS, status);
+  return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int4*)split, (const float*)part, out, Hq,
+                            G < F::HEADS ? G : F::HEADS);
 }
 
 int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }

@@ -353,7 +353,7 @@ struct PagedCfg {
   static constexpr int SLOT = CH * (CB + SB);
   static constexpr int SMEM = WARPS * SLOTS * SLOT;
 };
-constexpr int kMaxTile = 16;  // heads of a tile at most: a part is m[16], l[16], o[heads][D]
+constexpr int kMaxTile = 16;  // heads of a tile at most: a part is (m, l)[16], o[heads][D]
 __host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * kMaxTile; }
 
 // Position of 16-byte column `col` of a slot row, so that eight consecutive rows
@@ -404,6 +404,7 @@ constexpr int kItemUnits = 1;
 struct PagedParts {
   int n;
   int64_t size, longer;  // the first `longer` parts have size + 1 units
+  PagedParts() = default;
   __device__ __forceinline__ PagedParts(int64_t W, int warps) : n((int)min64(W, warps)), size(0), longer(0) {
     if (n == 0) return;
     size = W >> 31 ? W / n : (int)W / n;
@@ -440,7 +441,8 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
 template <int T, int D, int NC>
 __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     attn_paged_kernel(const ntx_paged_kv c, const float* __restrict__ q, int64_t qs, float* __restrict__ out,
-                      float* __restrict__ part, int Hq, const int* __restrict__ lens, float scale, int* status) {
+                      int4* __restrict__ split, float* __restrict__ part, int Hq, const int* __restrict__ lens,
+                      float scale, int* status) {
   using F = PagedCfg<T, D, NC>;
   constexpr int CH = F::CH, C = F::CB / 16, NB = D / 32, NS = CH / 16, NT = D / 16;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -457,6 +459,8 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
       for (int64_t i = lane; i < (int64_t)Hq * D / 4; i += 32)
         reinterpret_cast<float4*>(out + (int64_t)s * Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 
+  __shared__ PagedParts s_parts[F::WARPS];
+
   // ---- this warp's part: its first chunk, and `todo` units from there
   PagedCursor cur;
   int64_t todo;
@@ -465,7 +469,10 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     int64_t mine;
     const int64_t upto = lane_units(c, lens, k, CH, tiles, mine, status);
     const PagedParts parts(__shfl_sync(0xffffffffu, upto, 31), all_warps);
+    // what the parts of this warp's slots belong to, for the join: nothing yet
+    if (lane < 2) split[2 * wid + lane] = make_int4(0, 0, 0, 0);
     if (wid >= parts.n) return;
+    s_parts[warp] = parts;
     const int64_t u0 = parts.begin(wid);
     todo = parts.begin(wid + 1) - u0;
     const int at = __ffs(__ballot_sync(0xffffffffu, upto > u0)) - 1;  // the lane whose sequences hold u0
@@ -914,7 +921,15 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     if (item_end || todo <= 0) {
       const bool whole = item_end && item_head;
       // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
-      float* p = part + (2ll * wid + (item_head ? 1 : 0)) * paged_part_floats(min(F::HEADS, G), D);
+      const int64_t at = 2ll * wid + (item_head ? 1 : 0);
+      float* p = part + at * paged_part_floats(min(F::HEADS, G), D);
+      if (!whole && lane == 0) {  // the item's first warp and number of parts, where its output goes
+        const PagedParts parts = s_parts[warp];
+        // units up to the chunk after this one, less the item's own
+        const int64_t first = parts.begin(wid + 1) - max((int64_t)0, todo + (item_end ? kItemUnits : 0)) - cur.ci - 1;
+        const int w0 = parts.holder(first), n_parts = parts.holder(first + cur.n - 1) - w0 + 1;
+        split[at] = make_int4(w0, n_parts, cur.s, (head0 << 5) | rows);
+      }
 #pragma unroll
       for (int ct = 0; ct < NC; ++ct) {
         const int h = 4 * ct + t;
@@ -923,10 +938,7 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
         if (h >= rows) continue;
         float* dst = whole ? out + ((int64_t)cur.s * Hq + head0 + h) * D : p + 2 * kMaxTile + h * D;
         const float f = whole ? 1.f / l[ct] : 1.f;
-        if (!whole && g == 0) {
-          p[h] = m[ct];
-          p[kMaxTile + h] = l[ct];
-        }
+        if (!whole && g == 0) *reinterpret_cast<float2*>(p + 2 * h) = make_float2(m[ct], l[ct]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (T == kKvF16) {
@@ -947,12 +959,12 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
 }
 
 // Joins the parts of the items that several warps hold: with M the largest m,
-// out = sum 2^(m - M) o / sum 2^(m - M) l.  Which warps those are follows from the
-// lengths alone (read before the main kernel's end: no kernel of the call writes
-// them).  A warp takes 32 elements of an (item, head), four parts at a time; for
-// sequences of many parts a CTA does, 32 at a time.
+// out = sum 2^(m - M) o / sum 2^(m - M) l.  There is a CTA for every warp of the main
+// kernel, and an item's output is shared out among the CTAs of its parts.  By their
+// number a warp takes a head's whole row, all parts at once; or 32 elements of it,
+// four parts for every element; or a CTA 16 elements of it, 32 parts for every one.
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
-constexpr int kFewParts = 28;
+constexpr int kFewParts = 8, kManyParts = 64;
 constexpr int kMaxPagedSeqs = 1024;
 
 struct PagedMerge {  // a running join of parts, four elements a thread
@@ -969,32 +981,33 @@ struct PagedMerge {  // a running join of parts, four elements a thread
     L = fmaf(l, f, L);
     O.x = fmaf(o.x, f, O.x); O.y = fmaf(o.y, f, O.y); O.z = fmaf(o.z, f, O.z); O.w = fmaf(o.w, f, O.w);
   }
-  // parts first, first + step, ... below n; at(i) is part i, `row` and `e` the head and the element in it
-  template <int BATCH, class At>
+  // parts first, first + step, ... below n; at(i) is part i, e the four elements in it, of head `row`
+  template <class At>
   __device__ __forceinline__ void parts(At at, int first, int step, int n, int row, int e) {
+    constexpr int BATCH = 8;
     for (int i0 = first; i0 < n; i0 += step * BATCH) {
-      float m[BATCH], l[BATCH], top = M;
+      float2 ml[BATCH];
       float4 o[BATCH];
+      float top = M;
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
+        ml[b] = make_float2(-INFINITY, 0.f);
+        o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
         const int i = i0 + b * step;
-        const float* p = at(min(i, n - 1));
-        m[b] = i < n ? p[row] : -INFINITY;
-        l[b] = p[kMaxTile + row];
-        o[b] = *reinterpret_cast<const float4*>(p + e);
-        if (i >= n) {
-          l[b] = 0.f;
-          o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const float* p = at(i);
+          ml[b] = *reinterpret_cast<const float2*>(p + 2 * row);
+          o[b] = *reinterpret_cast<const float4*>(p + e);
         }
       }
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) top = fmaxf(top, m[b]);
+      for (int b = 0; b < BATCH; ++b) top = fmaxf(top, ml[b].x);
       scale_to(top);
 #pragma unroll
-      for (int b = 0; b < BATCH; ++b) add(m[b], l[b], o[b]);
+      for (int b = 0; b < BATCH; ++b) add(ml[b].x, ml[b].y, o[b]);
     }
   }
-  __device__ __forceinline__ void with_lane(int x) {  // and the parts of the lane `x` away
+  __device__ __forceinline__ void with_lane(int x) {  // and what the lane `x` away has
     scale_to(fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x)));
     L += __shfl_xor_sync(0xffffffffu, L, x);
     O.x += __shfl_xor_sync(0xffffffffu, O.x, x);
@@ -1002,121 +1015,74 @@ struct PagedMerge {  // a running join of parts, four elements a thread
     O.z += __shfl_xor_sync(0xffffffffu, O.z, x);
     O.w += __shfl_xor_sync(0xffffffffu, O.w, x);
   }
+  __device__ __forceinline__ void store(float* to) const {
+    const float f = 1.f / L;
+    *reinterpret_cast<float4*>(to) = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+  }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const ntx_paged_kv c, const float* part,
-                                                                      float* __restrict__ out, int Hq,
-                                                                      const int* __restrict__ lens, int ch,
-                                                                      int tile_heads, int all_warps, int* status) {
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  __shared__ __align__(16) float s_o[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = Hq / c.n_kv_heads, rtiles = (G + tile_heads - 1) / tile_heads, tiles = c.n_kv_heads * rtiles;
-  const int rows = min(tile_heads, G);
-  const int64_t stride = paged_part_floats(rows, D);
-  const int k = (c.n_seqs + 31) >> 5;  // sequences to a lane
-  int64_t mine;
-  const int64_t upto = lane_units(c, lens, k, ch, tiles, mine, status);
-  const PagedParts parts(__shfl_sync(0xffffffffu, upto, 31), all_warps);
-  auto chunks = [&](int s) { return (seq_len(c, lens, s, status) + ch - 1) / ch; };
-  auto many = [&](int n) { return n > kFewParts * parts.size; };
-
-  // (item, head, 32 elements) j of a sequence of n chunks: the parts' first warp and number, and the output
-  struct Unit {
-    int w0, cnt, r;
-    float* row;
-  };
-  constexpr int Z = D / 32;
-  const int per_seq = tiles * rows * Z;
-  auto unit = [&](int s, int n, int j) {
-    Unit u;
-    const int z = j % Z, tile = j / Z / rows;
-    u.r = j / Z - tile * rows;
-    const int kvh = tile / rtiles, h = (tile - kvh * rtiles) * tile_heads + u.r;
-    u.row = h < G ? out + ((int64_t)s * Hq + kvh * G + h) * D + 32 * z : nullptr;
-    const int holder = s / k;
-    int64_t first = __shfl_sync(0xffffffffu, upto - mine, holder);
-    for (int i = holder * k; i < s; ++i) first += (int64_t)item_units(chunks(i)) * tiles;
-    first += (int64_t)tile * item_units(n) + kItemUnits;
-    u.w0 = parts.holder(first);
-    u.cnt = parts.holder(first + n - 1) - u.w0 + 1;
-    return u;
-  };
-  // part i of an item: the first is in its warp's slot 1
-  auto part_of = [&](const Unit& u, int i) { return part + (2ll * (u.w0 + i) + (i == 0 ? 1 : 0)) * stride; };
-  bool waited = false;
-  auto wait = [&]() {
-    if (!waited) pdl_wait();
-    waited = true;
-  };
-
-  // the sequences of many parts: bit `lane` for each of the lane's sequences in turn
-  int n_many = 0;
-  for (int i = 0; i < k; ++i) {
-    const int s = lane * k + i;
-    n_many += __popc(__ballot_sync(0xffffffffu, s < c.n_seqs && many(chunks(s))));
-  }
-  for (int64_t x = blockIdx.x; x < (int64_t)n_many * per_seq; x += gridDim.x) {
-    int nth = (int)(x / per_seq), s = 0;
-    for (int i = 0; i < k; ++i) {
-      const int cand = lane * k + i;
-      unsigned mask = __ballot_sync(0xffffffffu, cand < c.n_seqs && many(chunks(cand)));
-      if (nth < __popc(mask)) {
-        for (; nth > 0; --nth) mask &= mask - 1;
-        s = (__ffs(mask) - 1) * k + i;
-        break;
-      }
-      nth -= __popc(mask);
-    }
-    const int j = (int)(x % per_seq);
-    const Unit u = unit(s, chunks(s), j);
-    if (!u.row) continue;
-    wait();
-    PagedMerge y;  // eight threads read the 32 elements of a part
-    y.parts<4>([&](int i) { return part_of(u, i); }, threadIdx.x >> 3, kJoinThreads / 8, u.cnt, u.r,
-               2 * kMaxTile + u.r * D + j % Z * 32 + lane % 8 * 4);
-    y.with_lane(8);
-    y.with_lane(16);
-    __syncthreads();  // the last unit's reads are done
-    if (lane < 8) *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = y.O;
-    if (lane == 0) {
-      s_m[warp] = y.M;
-      s_l[warp] = y.L;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      float M = s_m[0], sum = 0.f, tot = 0.f;
+__global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int4* split, const float* part,
+                                                                      float* __restrict__ out, int Hq, int rows_max) {
+  __shared__ float s_m[kJoinWarps][4], s_l[kJoinWarps][4];
+  __shared__ __align__(16) float4 s_o[kJoinWarps][4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.x;
+  const int64_t stride = paged_part_floats(rows_max, D);
+  pdl_wait();
+  const int4 both[2] = {split[2 * w], split[2 * w + 1]};
 #pragma unroll
-      for (int i = 1; i < kJoinWarps; ++i) M = fmaxf(M, s_m[i]);
-      if (M == -INFINITY) M = 0.f;
+  for (int k = 0; k < 2; ++k) {
+    const int4 it = both[k];  // first warp, parts, sequence, first head and number of heads
+    if (it.y == 0) continue;
+    const int heads = it.w & 31;
+    const float* base = part + 2ll * it.x * stride;  // the first part is in slot 1 of its warp, the others in slot 0
+    auto at = [&](int i) { return base + (2ll * i + (i == 0)) * stride; };
+    float* to = out + ((int64_t)it.z * Hq + (it.w >> 5)) * D;
+    if (it.y > kManyParts) {
+      constexpr int Z = D / 16;
+      for (int u = w - it.x; u < heads * Z; u += it.y) {
+        const int h = u / Z, e = h * D + u % Z * 16 + lane % 4 * 4;
+        PagedMerge y;
+        y.parts(at, threadIdx.x >> 2, kJoinThreads / 4, it.y, h, 2 * kMaxTile + e);
 #pragma unroll
-      for (int i = 0; i < kJoinWarps; ++i) {
-        const float f = ex2(s_m[i] - M);
-        sum = fmaf(s_o[i][lane], f, sum);
-        tot = fmaf(s_l[i], f, tot);
+        for (int o = 4; o < 32; o <<= 1) y.with_lane(o);
+        __syncthreads();  // the last unit's reads are done
+        if (lane < 4) {
+          s_o[warp][lane] = y.O;
+          s_m[warp][lane] = y.M;
+          s_l[warp][lane] = y.L;
+        }
+        __syncthreads();
+        if (threadIdx.x < 4) {
+          PagedMerge a;
+#pragma unroll
+          for (int i = 0; i < kJoinWarps; ++i) {
+            a.scale_to(fmaxf(a.M, s_m[i][lane]));
+            a.add(s_m[i][lane], s_l[i][lane], s_o[i][lane]);
+          }
+          a.store(to + e);
+        }
       }
-      u.row[lane] = sum / tot;
+    } else if (it.y > kFewParts) {
+      constexpr int Z = D / 32;
+      for (int u = (w - it.x) * kJoinWarps + warp; u < heads * Z; u += it.y * kJoinWarps) {
+        const int h = u / Z, e = h * D + u % Z * 32 + lane % 8 * 4;
+        PagedMerge y;
+        y.parts(at, lane >> 3, 4, it.y, h, 2 * kMaxTile + e);
+        y.with_lane(8);
+        y.with_lane(16);
+        if (lane < 8) y.store(to + e);
+      }
+    } else {
+      constexpr int ROW = D < 128 ? D : 128, Z = D / ROW;
+      for (int u = (w - it.x) * kJoinWarps + warp; u < heads * Z; u += it.y * kJoinWarps) {
+        const int h = u / Z, e = h * D + u % Z * ROW + lane % (ROW / 4) * 4;
+        PagedMerge y;
+        y.parts(at, 0, 1, it.y, h, 2 * kMaxTile + e);
+        if (lane < ROW / 4) y.store(to + e);
+      }
     }
   }
-
-  for (int64_t x = (int64_t)blockIdx.x * kJoinWarps + warp; x < (int64_t)c.n_seqs * per_seq;
-       x += (int64_t)gridDim.x * kJoinWarps) {
-    const int s = (int)(x >> 31 ? x / per_seq : (int)x / per_seq), j = (int)(x - (int64_t)s * per_seq), n = chunks(s);
-    if (n == 0 || many(n)) continue;
-    const Unit u = unit(s, n, j);
-    if (u.cnt < 2 || !u.row) continue;
-    wait();
-    PagedMerge y;
-    y.parts<4>([&](int i) { return part_of(u, i); }, lane >> 3, 4, u.cnt, u.r,
-               2 * kMaxTile + u.r * D + j % Z * 32 + lane % 8 * 4);
-    y.with_lane(8);
-    y.with_lane(16);
-    const float f = 1.f / y.L;
-    if (lane < 8)
-      *reinterpret_cast<float4*>(u.row + lane * 4) = make_float4(y.O.x * f, y.O.y * f, y.O.z * f, y.O.w * f);
-  }
-  wait();  // completion of this kernel implies the main kernel's
 }
 
 }  // namespace ntx
