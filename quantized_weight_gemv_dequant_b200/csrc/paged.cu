@@ -92,6 +92,12 @@ int check_tokens(const char* who, const ntx_paged_kv* kv, const float* k, const 
 
 bool rows16(const float* p, int64_t stride) { return aligned(p, 16) && stride % 4 == 0; }
 
+// Pieces of a token's row of keys (or values), and the grid over them: at most 512 pieces, 1024 heads of 256 elements.
+int token_pieces(const ntx_paged_kv* kv) { return (kv->n_kv_heads * kv->head_dim + kPiece - 1) / kPiece; }
+dim3 token_grid(int n_tokens, int pieces) {
+  return dim3((unsigned)(((int64_t)n_tokens + kTokenWarps - 1) / kTokenWarps), (unsigned)pieces);
+}
+
 template <class F>
 cudaError_t with_type(int type, F f) {
   switch (type) {
@@ -219,12 +225,33 @@ int ntx_qk_norm_rope(const float* q, const float* k, float* q_out, float* k_out,
   const uint64_t bq = span(n_tokens, q_stride, nq), bk = span(n_tokens, k_stride, nk);
   if ((nq && q != q_out && overlap(q, bq, q_out, bq)) || (nk && k != k_out && overlap(k, bk, k_out, bk)))
     return failf(NTX_ERR_INVALID_ARG, "%s: an output partially overlaps its input", who);
-  const int64_t rows = (int64_t)n_tokens * (n_q_heads + n_kv_heads);
-  const int grid = (int)min64((rows + 7) / 8, (int64_t)sm_count() * 8);
-  qk_norm_rope_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(q, k, q_out, k_out, q_stride, k_stride, wq, wk,
-                                                             positions, n_tokens, n_q_heads, n_kv_heads, head_dim,
-                                                             rot_dim, pairing, theta, eps);
-  return finish(who, cudaGetLastError());
+  const int heads = n_q_heads + n_kv_heads;
+  // whole rows of 64, 128 or 256 in 16-byte pieces; the halves' pairs are as wide apart as the lanes only when all rotate
+  const bool vec = (head_dim == 64 || head_dim == 128 || head_dim == 256) && rows16(q, q_stride) && rows16(k, k_stride) &&
+                   rows16(q_out, q_stride) && rows16(k_out, k_stride) &&
+                   (pairing == NTX_ROPE_ADJACENT || rot_dim == head_dim);
+  // log2(theta) as a number of 40 bits and the rest
+  const long double lg = std::log2((long double)theta);
+  const double lg_hi = (double)std::nearbyint(lg * 17179869184.0L) / 17179869184.0, lg_lo = (double)(lg - lg_hi);
+  const int64_t tiles = ((int64_t)n_tokens + kRopeTokens - 1) / kRopeTokens;
+  // CTAs for every tile up to the SMs' room, then shares of the heads until that room is filled
+  const int room = sm_count() * 4, gx = (int)min64(tiles, room);
+  const int most = (heads * (n_tokens < kRopeTokens ? n_tokens : kRopeTokens) + kRopeWarps - 1) / kRopeWarps;
+  const dim3 grid(gx, (unsigned)min64(most, room / gx));
+  auto run = [&](auto p, auto halves, auto v) {
+    qk_norm_rope_kernel<decltype(p)::value, decltype(halves)::value, decltype(v)::value>
+        <<<grid, kRopeWarps * 32, 0, (cudaStream_t)stream>>>(q, k, q_out, k_out, q_stride, k_stride, wq, wk, positions,
+                                                            n_tokens, n_q_heads, n_kv_heads, head_dim, rot_dim, lg_hi,
+                                                            lg_lo, eps);
+    return cudaGetLastError();
+  };
+  auto by_pairing = [&](auto p, auto v) {
+    return pairing == NTX_ROPE_HALVES ? run(p, std::true_type{}, v) : run(p, std::false_type{}, v);
+  };
+  auto by_vec = [&](auto p) { return vec ? by_pairing(p, std::true_type{}) : by_pairing(p, std::false_type{}); };
+  if (head_dim <= 64) return finish(who, by_vec(std::integral_constant<int, 1>{}));
+  if (head_dim <= 128) return finish(who, by_vec(std::integral_constant<int, 2>{}));
+  return finish(who, by_vec(std::integral_constant<int, 4>{}));
 }
 
 int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_t k_stride, int64_t v_stride,
@@ -234,10 +261,10 @@ int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_
   if (rc || n_tokens == 0) return rc;
   if (!k || !v) return failf(NTX_ERR_INVALID_ARG, "%s: NULL pointer", who);
   const bool vec = rows16(k, k_stride) && rows16(v, v_stride);
-  const dim3 grid((unsigned)min64(n_tokens, (int64_t)sm_count() * 64), 2);
+  const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
-    kv_append_kernel<decltype(t)::value><<<grid, 256, 0, (cudaStream_t)stream>>>(
-        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, device_status_ptr());
+    kv_append_kernel<decltype(t)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
     return cudaGetLastError();
   }));
 }
@@ -247,10 +274,11 @@ int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, in
   const char* who = "ntx_kv_read";
   const int rc = check_tokens(who, kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens);
   if (rc || n_tokens == 0 || (!k && !v)) return rc;
-  const dim3 grid((unsigned)min64(n_tokens, (int64_t)sm_count() * 64), 2);
+  const bool vec = (!k || rows16(k, k_stride)) && (!v || rows16(v, v_stride));
+  const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
-    kv_read_kernel<decltype(t)::value><<<grid, 256, 0, (cudaStream_t)stream>>>(
-        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, device_status_ptr());
+    kv_read_kernel<decltype(t)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
     return cudaGetLastError();
   }));
 }

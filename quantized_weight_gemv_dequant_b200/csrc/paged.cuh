@@ -42,181 +42,335 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
   return true;
 }
 
-// x rounded half away from zero, |x| < 2^22.
-__device__ __forceinline__ int round_away(float x) {
-  const float a = fabsf(x), f = floorf(a);
-  const int t = (int)f + (a - f >= 0.5f ? 1 : 0);  // a - f is exact
-  return x < 0.f ? -t : t;
-}
+// A warp of the write and of the read handles one row's piece of kPiece elements,
+// four consecutive ones to a lane at a time (eight lanes a block of 32), all its
+// loads in flight at once.  Both kernels are bound by memory; a row's place is
+// looked up once a piece.
+constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
+constexpr int kTokenWarps = 8;  // tokens of a CTA
 
 // ------------------------------------------------------------- cache write
-// Eight lanes hold one block of 32, four consecutive elements each.
+// fp32 quotient w / d rounded half away from zero, from r close to 1 / d: only a
+// product next to a half needs the quotient itself.  |w r - w / d| is below
+// 2 steps of 2^-24 times 127 (the largest quotient is 127, or 8), so below 2^-15.
+__device__ __forceinline__ int quotient_round(float w, float d, float r) {
+  float x = fabsf(w * r);
+  float f = floorf(x);
+  if (!(x < 256.f) || fabsf(x - f - 0.5f) < 0x1p-14f) {
+    x = fabsf(w / d);
+    f = floorf(x);
+  }
+  const int t = (int)f + (x - f >= 0.5f ? 1 : 0);  // x - f is exact
+  return (w < 0.f) != (d < 0.f) ? -t : t;
+}
+
 template <int T>
-__global__ void __launch_bounds__(256) kv_append_kernel(const ntx_paged_kv c, const float* __restrict__ k,
-                                                        const float* __restrict__ v, int64_t ks, int64_t vs,
-                                                        const int* __restrict__ seq_ids,
-                                                        const int* __restrict__ positions, int n_tokens, bool vec,
-                                                        int* status) {
-  const int D = c.head_dim, nb = D >> 5, row_blocks = c.n_kv_heads * nb;
-  const int sub = threadIdx.x & 7;
-  const float* src = blockIdx.y ? v : k;
-  const int64_t stride = blockIdx.y ? vs : ks;
-  uint8_t* pool = static_cast<uint8_t*>(blockIdx.y ? c.v_pages : c.k_pages);
-  const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D);
-  for (int n = blockIdx.x; n < n_tokens; n += gridDim.x) {
-    const int pos = __ldg(positions + n);
-    if (pos < 0) continue;
-    int64_t page;
-    int row;
-    if (!kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) continue;
-    const float* in = src + n * stride;
-    for (int b0 = 0; b0 < row_blocks; b0 += 32) {  // the 32 blocks of the CTA's 256 threads
-      const int b = b0 + (threadIdx.x >> 3);
-      const bool on = b < row_blocks;
-      float w[4] = {0.f, 0.f, 0.f, 0.f};
-      if (on) {
-        const float* p = in + b * 32 + sub * 4;
-        if (vec) {
-          const float4 t = *reinterpret_cast<const float4*>(p);
-          w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
-        } else {
+__global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_paged_kv c, const float* __restrict__ k,
+                                                                     const float* __restrict__ v, int64_t ks,
+                                                                     int64_t vs, const int* __restrict__ seq_ids,
+                                                                     const int* __restrict__ positions, int n_tokens,
+                                                                     bool vec, int pieces, int* status) {
+  const int D = c.head_dim, nb = D >> 5, width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
+  const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
+  if (n >= n_tokens) return;
+  const int piece = (int)blockIdx.y % pieces, e0 = piece * kPiece + lane * 4;
+  const bool is_v = (int)blockIdx.y >= pieces;
+  const float* in = is_v ? v + n * vs : k + n * ks;
+  const int pos = __ldg(positions + n);
+  float w[kPieceSteps][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = p[i];
-        }
-      }
-      const int head = b / nb, blk = b - head * nb;
-      uint8_t* part = pool + (page * c.n_kv_heads + head) * head_bytes;
-      if constexpr (T == kKvF16) {
-        if (on) {
-          uint2 h;
-          h.x = float_to_half_bits(w[0]) | ((uint32_t)float_to_half_bits(w[1]) << 16);
-          h.y = float_to_half_bits(w[2]) | ((uint32_t)float_to_half_bits(w[3]) << 16);
-          *reinterpret_cast<uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2) = h;
-        }
+  for (int i = 0; i < kPieceSteps; ++i) {
+    const int e = e0 + i * 128;
+    w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0.f;
+    if (e < width) {
+      if (vec) {
+        const float4 t = *reinterpret_cast<const float4*>(in + e);
+        w[i][0] = t.x; w[i][1] = t.y; w[i][2] = t.z; w[i][3] = t.w;
       } else {
-        // |w| as ordered bits: the largest, and whether any is not finite
-        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool finite = top < 0x7F800000u;
-        float d;
-        if constexpr (T == kKvQ8) {
-          d = __uint_as_float(top) / 127.0f;
-        } else {
-          // the first element of the largest magnitude decides the sign
-          int key = 64;
-#pragma unroll
-          for (int i = 3; i >= 0; --i)
-            if ((__float_as_uint(w[i]) & 0x7FFFFFFFu) == top) key = 2 * (4 * sub + i) + (w[i] < 0.f ? 1 : 0);
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
-          const float m = (key & 1) ? -__uint_as_float(top) : __uint_as_float(top);
-          d = m * -0.125f;
-        }
-        const bool zero = top == 0 || !finite;
-        int q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = zero ? 0 : round_away(w[i] / d);
-          q[i] = T == kKvQ8 ? min(127, max(-127, r)) : min(15, max(0, r + 8));
-        }
-        const uint32_t codes = (q[0] & 255) | ((q[1] & 255) << 8) | ((q[2] & 255) << 16) | ((uint32_t)(q[3] & 255) << 24);
-        if constexpr (T == kKvQ8) {
-          if (on) *reinterpret_cast<uint32_t*>(part + (int64_t)row * D + blk * 32 + sub * 4) = codes;
-        } else {
-          const uint32_t hi = __shfl_down_sync(0xffffffffu, codes, 4, 8);  // elements 16 further on
-          if (on && sub < 4)
-            *reinterpret_cast<uint32_t*>(part + (int64_t)row * (D / 2) + blk * 16 + sub * 4) = codes | (hi << 4);
-        }
-        if (on && sub == 0)
-          *reinterpret_cast<uint16_t*>(part + (int64_t)c.page_size * kv_code_bytes<T>(D) + ((int64_t)row * nb + blk) * 2) =
-              finite ? float_to_half_bits(d) : (uint16_t)0x7FFF;
+        for (int j = 0; j < 4; ++j) w[i][j] = in[e + j];
       }
+    }
+  }
+  int64_t page;
+  int row;
+  if (pos < 0 || !kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) return;
+  uint8_t* part0 = static_cast<uint8_t*>(is_v ? c.v_pages : c.k_pages) +
+                   page * c.n_kv_heads * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+#pragma unroll
+  for (int i = 0; i < kPieceSteps; ++i) {
+    const int e = e0 + i * 128;
+    if (e - lane * 4 >= width) break;
+    const bool on = e < width;
+    const int head = e / D, blk = (e - head * D) >> 5;
+    uint8_t* part = part0 + head * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+    if constexpr (T == kKvF16) {
+      if (on) {
+        uint2 h;
+        h.x = float_to_half_bits(w[i][0]) | ((uint32_t)float_to_half_bits(w[i][1]) << 16);
+        h.y = float_to_half_bits(w[i][2]) | ((uint32_t)float_to_half_bits(w[i][3]) << 16);
+        *reinterpret_cast<uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2) = h;
+      }
+    } else {
+      // |w| as ordered bits: the block's largest, and whether any is not finite
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(w[i][j]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < 0x7F800000u;
+      float d;
+      if constexpr (T == kKvQ8) {
+        d = __uint_as_float(top) / 127.0f;
+      } else {
+        // the first element of the largest magnitude decides the sign
+        int key = 64;
+#pragma unroll
+        for (int j = 3; j >= 0; --j)
+          if ((__float_as_uint(w[i][j]) & 0x7FFFFFFFu) == top) key = 2 * (4 * sub + j) + (w[i][j] < 0.f ? 1 : 0);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
+        d = ((key & 1) ? -__uint_as_float(top) : __uint_as_float(top)) * -0.125f;
+      }
+      const bool zero = top == 0 || !finite;
+      const float r = 1.0f / d;
+      uint32_t codes = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = zero ? 0 : quotient_round(w[i][j], d, r);
+        codes |= (uint32_t)((T == kKvQ8 ? min(127, max(-127, q)) : min(15, max(0, q + 8))) & 255) << (8 * j);
+      }
+      if constexpr (T == kKvQ8) {
+        if (on) *reinterpret_cast<uint32_t*>(part + (int64_t)row * D + blk * 32 + sub * 4) = codes;
+      } else {
+        const uint32_t hi = __shfl_down_sync(0xffffffffu, codes, 4, 8);  // elements 16 further on
+        if (on && sub < 4)
+          *reinterpret_cast<uint32_t*>(part + (int64_t)row * (D / 2) + blk * 16 + sub * 4) = codes | (hi << 4);
+      }
+      if (on && sub == 0)
+        *reinterpret_cast<uint16_t*>(part + (int64_t)c.page_size * kv_code_bytes<T>(D) + ((int64_t)row * nb + blk) * 2) =
+            finite ? float_to_half_bits(d) : (uint16_t)0x7FFF;
     }
   }
 }
 
 // ------------------------------------------------------------- cache read
 template <int T>
-__device__ __forceinline__ float kv_element(const uint8_t* part, int page_size, int D, int row, int e) {
-  if constexpr (T == kKvF16) {
-    return half_bits_to_float(*reinterpret_cast<const uint16_t*>(part + ((int64_t)row * D + e) * 2));
-  } else {
-    const float d = half_bits_to_float(*reinterpret_cast<const uint16_t*>(
-        part + (int64_t)page_size * kv_code_bytes<T>(D) + ((int64_t)row * (D >> 5) + (e >> 5)) * 2));
-    if constexpr (T == kKvQ8) return d * (float)(int8_t)part[(int64_t)row * D + e];
-    const int byte = part[(int64_t)row * (D / 2) + (e >> 5) * 16 + (e & 15)];
-    return d * (float)(((e & 16) ? byte >> 4 : byte & 15) - 8);
+__global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_paged_kv c, float* __restrict__ k,
+                                                                   float* __restrict__ v, int64_t ks, int64_t vs,
+                                                                   const int* __restrict__ seq_ids,
+                                                                   const int* __restrict__ positions, int n_tokens,
+                                                                   bool vec, int pieces, int* status) {
+  const int D = c.head_dim, nb = D >> 5, width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
+  const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
+  if (n >= n_tokens) return;
+  const int piece = (int)blockIdx.y % pieces, e0 = piece * kPiece + lane * 4;
+  const bool is_v = (int)blockIdx.y >= pieces;
+  if (!(is_v ? v : k)) return;
+  float* out = is_v ? v + n * vs : k + n * ks;
+  const int pos = __ldg(positions + n);
+  int64_t page;
+  int row;
+  if (pos < 0 || !kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) return;
+  const uint8_t* part0 = static_cast<const uint8_t*>(is_v ? c.v_pages : c.k_pages) +
+                         page * c.n_kv_heads * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+  uint2 code[kPieceSteps];
+  uint16_t scale[kPieceSteps];
+#pragma unroll
+  for (int i = 0; i < kPieceSteps; ++i) {
+    const int e = e0 + i * 128;
+    if (e >= width) break;
+    const int head = e / D, blk = (e - head * D) >> 5;
+    const uint8_t* part = part0 + head * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+    if constexpr (T == kKvF16) {
+      code[i] = __ldcs(reinterpret_cast<const uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2));
+    } else {
+      const int at = T == kKvQ8 ? blk * 32 + sub * 4 : blk * 16 + (sub & 3) * 4;
+      code[i].x = *reinterpret_cast<const uint32_t*>(part + (int64_t)row * kv_code_bytes<T>(D) + at);
+      scale[i] = *reinterpret_cast<const uint16_t*>(part + (int64_t)c.page_size * kv_code_bytes<T>(D) +
+                                                    ((int64_t)row * nb + blk) * 2);
+    }
   }
-}
-
-template <int T>
-__global__ void __launch_bounds__(256) kv_read_kernel(const ntx_paged_kv c, float* __restrict__ k,
-                                                      float* __restrict__ v, int64_t ks, int64_t vs,
-                                                      const int* __restrict__ seq_ids,
-                                                      const int* __restrict__ positions, int n_tokens, int* status) {
-  const int D = c.head_dim;
-  float* dst = blockIdx.y ? v : k;
-  if (!dst) return;
-  const int64_t stride = blockIdx.y ? vs : ks;
-  const uint8_t* pool = static_cast<const uint8_t*>(blockIdx.y ? c.v_pages : c.k_pages);
-  const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D);
-  for (int n = blockIdx.x; n < n_tokens; n += gridDim.x) {
-    const int pos = __ldg(positions + n);
-    if (pos < 0) continue;
-    int64_t page;
-    int row;
-    if (!kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) continue;
-    for (int e = threadIdx.x; e < c.n_kv_heads * D; e += blockDim.x) {
-      const int head = e / D;
-      dst[n * stride + e] =
-          kv_element<T>(pool + (page * c.n_kv_heads + head) * head_bytes, c.page_size, D, row, e - head * D);
+#pragma unroll
+  for (int i = 0; i < kPieceSteps; ++i) {
+    const int e = e0 + i * 128;
+    if (e >= width) break;
+    float4 o;
+    if constexpr (T == kKvF16) {
+      o = make_float4(half_bits_to_float(code[i].x), half_bits_to_float(code[i].x >> 16),
+                      half_bits_to_float(code[i].y), half_bits_to_float(code[i].y >> 16));
+    } else {
+      const float d = half_bits_to_float(scale[i]);
+      uint32_t u = code[i].x;
+      if constexpr (T == kKvQ8) {
+        o = make_float4((int8_t)u, (int8_t)(u >> 8), (int8_t)(u >> 16), (int8_t)(u >> 24));
+      } else {
+        u = sub < 4 ? u : u >> 4;
+        o = make_float4((int)(u & 15) - 8, (int)(u >> 8 & 15) - 8, (int)(u >> 16 & 15) - 8, (int)(u >> 24 & 15) - 8);
+      }
+      o.x *= d; o.y *= d; o.z *= d; o.w *= d;  // exact: 11 by 8 bits
+    }
+    if (vec) {
+      *reinterpret_cast<float4*>(out + e) = o;
+    } else {
+      out[e] = o.x; out[e + 1] = o.y; out[e + 2] = o.z; out[e + 3] = o.w;
     }
   }
 }
 
 // ------------------------------------------------------------- head norm + rotation
-// One warp per (token, head).
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const float* q, const float* k, float* q_out, float* k_out,
-                                                           int64_t qs, int64_t ks, const float* __restrict__ wq,
-                                                           const float* __restrict__ wk,
-                                                           const int* __restrict__ positions, int n_tokens, int Hq,
-                                                           int Hkv, int D, int R, int halves, float theta, float eps) {
-  __shared__ float rows[8][256];
-  const int lane = threadIdx.x & 31, heads = Hq + Hkv;
-  float* x = rows[threadIdx.x >> 5];
-  const int64_t total = (int64_t)n_tokens * heads;
-  for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < total; i += gridDim.x * 8ll) {
-    const int n = (int)(i / heads), h = (int)(i - (int64_t)n * heads);
-    const int pos = __ldg(positions + n);
-    if (pos < 0) continue;
-    const bool is_q = h < Hq;
-    const int64_t at = is_q ? n * qs + (int64_t)h * D : n * ks + (int64_t)(h - Hq) * D;
-    const float* in = (is_q ? q : k) + at;
-    float* out = (is_q ? q_out : k_out) + at;
-    const float* w = is_q ? wq : wk;
-    float ss = 0.f;
-    for (int e = lane; e < D; e += 32) {
-      const float t = in[e];
-      x[e] = t;
-      ss = fmaf(t, t, ss);
+// theta^(-2p/R) to fp64's precision: 2^-x with x = 2p log2(theta) / R as a quotient
+// and its remainder (log2 theta in two numbers, the first of 40 bits, so that 2p
+// times it is exact).
+__device__ __forceinline__ double rope_frequency(int p, int R, double log2_hi, double log2_lo) {
+  const double a = 2.0 * p * log2_hi, q = a / R;
+  const double rest = (fma(-q, (double)R, a) + 2.0 * p * log2_lo) / R;
+  return exp2(-q) * (1.0 - 0.69314718055994530942 * rest);
+}
+
+// A CTA takes tiles of kRopeTokens tokens and a share of their heads: its threads
+// form the tile's cosines and sines once, in fp64 (the angle in half turns, so that
+// its reduction is exact), and each warp norms and rotates the heads' rows, several
+// in flight.  Bound by memory.  VEC: rows are 16-byte aligned and a lane holds P
+// consecutive pairs; otherwise pairs lane, lane + 32, ...
+constexpr int kRopeTokens = 4, kRopeWarps = 8;
+template <int P, bool HALVES, bool VEC>
+__global__ void __launch_bounds__(kRopeWarps * 32)
+    qk_norm_rope_kernel(const float* q, const float* k, float* q_out, float* k_out, int64_t qs, int64_t ks,
+                        const float* __restrict__ wq, const float* __restrict__ wk, const int* __restrict__ positions,
+                        int n_tokens, int Hq, int Hkv, int D, int R, double log2_hi, double log2_lo, float eps) {
+  // A row's elements as D / 2 pairs: the R / 2 that rotate, then neighbours.  A lane's pairs:
+  constexpr int U = VEC ? 4 : 2;  // rows in flight
+  __shared__ float2 turn[kRopeTokens][32 * P];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = Hq + Hkv, half = R / 2;
+  auto pair = [&](int i) { return VEC ? lane * P + i : lane + 32 * i; };
+  auto first = [&](int p) { return HALVES && p < half ? p : 2 * p; };
+  auto second = [&](int p) { return HALVES && p < half ? p + half : 2 * p + 1; };
+  const int my_pair = threadIdx.x % (32 * P), my_token = threadIdx.x / (32 * P);
+  const double f = my_pair < half ? rope_frequency(my_pair, R, log2_hi, log2_lo) * 0.31830988618379067154 : 0.0;
+  float w[2][P][2];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = pair(i);
+    const bool on = 2 * p < D;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float* wt = x ? wk : wq;
+      w[x][i][0] = on && wt ? __ldg(wt + first(p)) : 1.f;
+      w[x][i][1] = on && wt ? __ldg(wt + second(p)) : 1.f;
     }
-    const float r = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
-    __syncwarp();
-    for (int e = lane; e < D; e += 32) x[e] = (x[e] * r) * (w ? __ldg(w + e) : 1.f);
-    __syncwarp();
-    for (int p = lane; p < R / 2; p += 32) {
-      const int e0 = halves ? p : 2 * p, e1 = halves ? p + R / 2 : 2 * p + 1;
+  }
+  for (int64_t tile = blockIdx.x; tile * kRopeTokens < n_tokens; tile += gridDim.x) {
+    const int n0 = (int)(tile * kRopeTokens), tokens = min(kRopeTokens, n_tokens - n0), rows = tokens * heads;
+    __syncthreads();
+    for (int n = my_token; n < tokens; n += kRopeWarps / P) {
       double s, c;
-      sincos((double)pos * pow((double)theta, -2.0 * p / R), &s, &c);
-      const float a = x[e0], b = x[e1];
-      out[e0] = a * (float)c - b * (float)s;
-      out[e1] = a * (float)s + b * (float)c;
+      sincospi(f * __ldg(positions + n0 + n), &s, &c);
+      turn[n][my_pair] = make_float2((float)c, (float)s);
     }
-    for (int e = R + lane; e < D; e += 32) out[e] = x[e];
-    __syncwarp();
+    __syncthreads();
+    for (int r0 = (blockIdx.y * kRopeWarps + warp) * U; r0 < rows; r0 += gridDim.y * kRopeWarps * U) {
+      float x[U][P][2];
+      int64_t at[U];
+      int token[U];
+      bool is_q[U], live[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u;
+        token[u] = min(r, rows - 1) / heads;
+        const int h = min(r, rows - 1) - token[u] * heads, n = n0 + token[u];
+        is_q[u] = h < Hq;
+        at[u] = is_q[u] ? n * qs + (int64_t)h * D : n * ks + (int64_t)(h - Hq) * D;
+        live[u] = r < rows && __ldg(positions + n) >= 0;
+        const float* in = (is_q[u] ? q : k) + at[u];
+        if (!live[u]) continue;
+        if constexpr (VEC && HALVES) {
+          if constexpr (P == 1) {
+            x[u][0][0] = in[lane];
+            x[u][0][1] = in[lane + 32];
+          } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+              const float2 a = *reinterpret_cast<const float2*>(in + lane * P + i);
+              const float2 b = *reinterpret_cast<const float2*>(in + 32 * P + lane * P + i);
+              x[u][i][0] = a.x; x[u][i + 1][0] = a.y;
+              x[u][i][1] = b.x; x[u][i + 1][1] = b.y;
+            }
+          }
+        } else if constexpr (VEC) {
+          if constexpr (P == 1) {
+            const float2 a = *reinterpret_cast<const float2*>(in + 2 * lane);
+            x[u][0][0] = a.x; x[u][0][1] = a.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+              const float4 a = *reinterpret_cast<const float4*>(in + 2 * (lane * P + i));
+              x[u][i][0] = a.x; x[u][i][1] = a.y;
+              x[u][i + 1][0] = a.z; x[u][i + 1][1] = a.w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int p = pair(i);
+            x[u][i][0] = 2 * p < D ? in[first(p)] : 0.f;
+            x[u][i][1] = 2 * p < D ? in[second(p)] : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!live[u]) continue;  // (the same in the whole warp)
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) ss = fmaf(x[u][i][0], x[u][i][0], fmaf(x[u][i][1], x[u][i][1], ss));
+        const float norm = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
+        float* out = (is_q[u] ? q_out : k_out) + at[u];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int p = pair(i);
+          const float a = x[u][i][0] * norm * (is_q[u] ? w[0][i][0] : w[1][i][0]);
+          const float b = x[u][i][1] * norm * (is_q[u] ? w[0][i][1] : w[1][i][1]);
+          const float2 t = p < half ? turn[token[u]][p] : make_float2(1.f, 0.f);
+          x[u][i][0] = a * t.x - b * t.y;
+          x[u][i][1] = a * t.y + b * t.x;
+          if (p >= half) {  // only normed: as it is, infinities too
+            x[u][i][0] = a;
+            x[u][i][1] = b;
+          }
+        }
+        if constexpr (VEC && HALVES) {
+          if constexpr (P == 1) {
+            out[lane] = x[u][0][0];
+            out[lane + 32] = x[u][0][1];
+          } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+              *reinterpret_cast<float2*>(out + lane * P + i) = make_float2(x[u][i][0], x[u][i + 1][0]);
+              *reinterpret_cast<float2*>(out + 32 * P + lane * P + i) = make_float2(x[u][i][1], x[u][i + 1][1]);
+            }
+          }
+        } else if constexpr (VEC) {
+          if constexpr (P == 1) {
+            *reinterpret_cast<float2*>(out + 2 * lane) = make_float2(x[u][0][0], x[u][0][1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2)
+              *reinterpret_cast<float4*>(out + 2 * (lane * P + i)) =
+                  make_float4(x[u][i][0], x[u][i][1], x[u][i + 1][0], x[u][i + 1][1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int p = pair(i);
+            if (2 * p < D) {
+              out[first(p)] = x[u][i][0];
+              out[second(p)] = x[u][i][1];
+            }
+          }
+        }
+      }
+    }
   }
 }
 
