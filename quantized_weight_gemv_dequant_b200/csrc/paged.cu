@@ -233,16 +233,18 @@ int ntx_qk_norm_rope(const float* q, const float* k, float* q_out, float* k_out,
   // log2(theta) as a number of 40 bits and the rest
   const long double lg = std::log2((long double)theta);
   const double lg_hi = (double)std::nearbyint(lg * 17179869184.0L) / 17179869184.0, lg_lo = (double)(lg - lg_hi);
-  const int64_t tiles = ((int64_t)n_tokens + kRopeTokens - 1) / kRopeTokens;
-  // CTAs for every tile up to the SMs' room, then shares of the heads until that room is filled
-  const int room = sm_count() * 4, gx = (int)min64(tiles, room);
-  const int most = (heads * (n_tokens < kRopeTokens ? n_tokens : kRopeTokens) + kRopeWarps - 1) / kRopeWarps;
-  const dim3 grid(gx, (unsigned)min64(most, room / gx));
+  // Rows of a token that a warp takes: enough shares for eight rounds of the warps that the SMs hold, one row at
+  // least, all at most; fours where there are as many, which is what a warp has in flight.
+  const int room = sm_count() * rope_ctas(head_dim <= 128 ? 1 : 4);
+  int rows = (int)min64(heads, (int64_t)n_tokens * heads / ((int64_t)room * kRopeWarps * 8) + 1);
+  if (rows > 4) rows = (rows + 3) / 4 * 4;
+  const int shares = (heads + rows - 1) / rows;
+  const int grid = (int)min64(((int64_t)n_tokens * shares + kRopeWarps - 1) / kRopeWarps, room);
   auto run = [&](auto p, auto halves, auto v) {
     qk_norm_rope_kernel<decltype(p)::value, decltype(halves)::value, decltype(v)::value>
         <<<grid, kRopeWarps * 32, 0, (cudaStream_t)stream>>>(q, k, q_out, k_out, q_stride, k_stride, wq, wk, positions,
                                                             n_tokens, n_q_heads, n_kv_heads, head_dim, rot_dim, lg_hi,
-                                                            lg_lo, eps);
+                                                            lg_lo, eps, rows, shares);
     return cudaGetLastError();
   };
   auto by_pairing = [&](auto p, auto v) {
@@ -263,9 +265,11 @@ int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_
   const bool vec = rows16(k, k_stride) && rows16(v, v_stride);
   const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
-    kv_append_kernel<decltype(t)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+    return with_dim(kv->head_dim, [&](auto d) {
+    kv_append_kernel<decltype(t)::value, decltype(d)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
         *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
     return cudaGetLastError();
+    });
   }));
 }
 
@@ -277,9 +281,11 @@ int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, in
   const bool vec = (!k || rows16(k, k_stride)) && (!v || rows16(v, v_stride));
   const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
-    kv_read_kernel<decltype(t)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+    return with_dim(kv->head_dim, [&](auto d) {
+    kv_read_kernel<decltype(t)::value, decltype(d)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
         *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
     return cudaGetLastError();
+    });
   }));
 }
 

@@ -47,30 +47,54 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 // loads in flight at once.  Both kernels are bound by memory; a row's place is
 // looked up once a piece.
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
-constexpr int kTokenWarps = 8;  // tokens of a CTA
+constexpr int kTokenWarps = 4;  // tokens of a CTA
 
 // ------------------------------------------------------------- cache write
-// fp32 quotient w / d rounded half away from zero, from r close to 1 / d: only a
-// product next to a half needs the quotient itself.  |w r - w / d| is below
-// 2 steps of 2^-24 times 127 (the largest quotient is 127, or 8), so below 2^-15.
-__device__ __forceinline__ int quotient_round(float w, float d, float r) {
-  float x = fabsf(w * r);
-  float f = floorf(x);
-  if (!(x < 256.f) || fabsf(x - f - 0.5f) < 0x1p-14f) {
-    x = fabsf(w / d);
-    f = floorf(x);
+// A code is the fp32 quotient w / d rounded half away from zero.  w times rcp(d),
+// within 2^-14 of the quotient (which is at most 127, or 8), tells it unless it is
+// next to a half; rounding is by adding 1.5 2^23 (and 8 for Q4_0), whose lowest
+// byte is then the code.  Next to a half, and where rcp(d) overflows, the quotient
+// itself decides.
+template <int T>
+__device__ __forceinline__ uint32_t quotient_code(float w, float d) {
+  const float x = fabsf(w / d), f = floorf(x);
+  int q = (int)f + (x - f >= 0.5f ? 1 : 0);  // x - f is exact
+  q = (w < 0.f) != (d < 0.f) ? -q : q;
+  return (uint32_t)(T == kKvQ8 ? min(127, max(-127, q)) : min(15, max(0, q + 8))) & 255u;
+}
+template <int T>
+__device__ __forceinline__ uint32_t quotient_codes(const float w[4], float d) {
+  constexpr float kMagic = T == kKvQ8 ? 12582912.f : 12582920.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  uint32_t m[4];
+  bool sure = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = w[i] * r, y = x + kMagic;
+    sure &= fabsf(x - (y - kMagic)) < 0.5f - 0x1p-14f;
+    m[i] = __float_as_uint(T == kKvQ4 ? fminf(y, kMagic + 7.f) : y);
   }
-  const int t = (int)f + (x - f >= 0.5f ? 1 : 0);  // x - f is exact
-  return (w < 0.f) != (d < 0.f) ? -t : t;
+  if (sure) return __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) codes |= quotient_code<T>(w[i], d) << (8 * i);
+  return codes;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
 }
 
-template <int T>
+template <int T, int D>
 __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_paged_kv c, const float* __restrict__ k,
                                                                      const float* __restrict__ v, int64_t ks,
                                                                      int64_t vs, const int* __restrict__ seq_ids,
                                                                      const int* __restrict__ positions, int n_tokens,
                                                                      bool vec, int pieces, int* status) {
-  const int D = c.head_dim, nb = D >> 5, width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
+  constexpr int nb = D / 32;
+  const int width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
   const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
   if (n >= n_tokens) return;
   const int piece = (int)blockIdx.y % pieces, e0 = piece * kPiece + lane * 4;
@@ -112,34 +136,29 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
         *reinterpret_cast<uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2) = h;
       }
     } else {
-      // |w| as ordered bits: the block's largest, and whether any is not finite
-      uint32_t top = 0;
+      float top = max_nan(max_nan(fabsf(w[i][0]), fabsf(w[i][1])), max_nan(fabsf(w[i][2]), fabsf(w[i][3])));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(w[i][j]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool finite = top < 0x7F800000u;
+      for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < INFINITY;
       float d;
       if constexpr (T == kKvQ8) {
-        d = __uint_as_float(top) / 127.0f;
+        d = top / 127.0f;
       } else {
         // the first element of the largest magnitude decides the sign
-        int key = 64;
+        float m = 0.f;
+        bool has = false;
 #pragma unroll
         for (int j = 3; j >= 0; --j)
-          if ((__float_as_uint(w[i][j]) & 0x7FFFFFFFu) == top) key = 2 * (4 * sub + j) + (w[i][j] < 0.f ? 1 : 0);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
-        d = ((key & 1) ? -__uint_as_float(top) : __uint_as_float(top)) * -0.125f;
+          if (fabsf(w[i][j]) == top) {
+            m = w[i][j];
+            has = true;
+          }
+        const unsigned lanes = __ballot_sync(0xffffffffu, has) >> (lane & 24) & 255u;
+        m = __shfl_sync(0xffffffffu, m, (lane & 24) + (lanes ? __ffs(lanes) - 1 : 0));
+        d = (top > 0.f ? m : 0.f) * -0.125f;
       }
-      const bool zero = top == 0 || !finite;
-      const float r = 1.0f / d;
-      uint32_t codes = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int q = zero ? 0 : quotient_round(w[i][j], d, r);
-        codes |= (uint32_t)((T == kKvQ8 ? min(127, max(-127, q)) : min(15, max(0, q + 8))) & 255) << (8 * j);
-      }
+      // zeros and blocks that are not finite: codes of zero
+      const uint32_t codes = top > 0.f && finite ? quotient_codes<T>(w[i], d) : T == kKvQ8 ? 0u : 0x08080808u;
       if constexpr (T == kKvQ8) {
         if (on) *reinterpret_cast<uint32_t*>(part + (int64_t)row * D + blk * 32 + sub * 4) = codes;
       } else {
@@ -155,13 +174,14 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
 }
 
 // ------------------------------------------------------------- cache read
-template <int T>
+template <int T, int D>
 __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_paged_kv c, float* __restrict__ k,
                                                                    float* __restrict__ v, int64_t ks, int64_t vs,
                                                                    const int* __restrict__ seq_ids,
                                                                    const int* __restrict__ positions, int n_tokens,
                                                                    bool vec, int pieces, int* status) {
-  const int D = c.head_dim, nb = D >> 5, width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
+  constexpr int nb = D / 32;
+  const int width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
   const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
   if (n >= n_tokens) return;
   const int piece = (int)blockIdx.y % pieces, e0 = piece * kPiece + lane * 4;
@@ -201,13 +221,9 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_pag
                       half_bits_to_float(code[i].y), half_bits_to_float(code[i].y >> 16));
     } else {
       const float d = half_bits_to_float(scale[i]);
-      uint32_t u = code[i].x;
-      if constexpr (T == kKvQ8) {
-        o = make_float4((int8_t)u, (int8_t)(u >> 8), (int8_t)(u >> 16), (int8_t)(u >> 24));
-      } else {
-        u = sub < 4 ? u : u >> 4;
-        o = make_float4((int)(u & 15) - 8, (int)(u >> 8 & 15) - 8, (int)(u >> 16 & 15) - 8, (int)(u >> 24 & 15) - 8);
-      }
+      constexpr float off = 8388608.f + (T == kKvQ8 ? 128.f : 8.f);  // magic_byte gives 2^23 + u
+      const uint32_t u = T == kKvQ8 ? code[i].x ^ 0x80808080u : (code[i].x >> (sub & 4)) & 0x0F0F0F0Fu;
+      o = make_float4(magic_byte<0>(u) - off, magic_byte<1>(u) - off, magic_byte<2>(u) - off, magic_byte<3>(u) - off);
       o.x *= d; o.y *= d; o.z *= d; o.w *= d;  // exact: 11 by 8 bits
     }
     if (vec) {
@@ -228,30 +244,31 @@ __device__ __forceinline__ double rope_frequency(int p, int R, double log2_hi, d
   return exp2(-q) * (1.0 - 0.69314718055994530942 * rest);
 }
 
-// A CTA takes tiles of kRopeTokens tokens and a share of their heads: its threads
-// form the tile's cosines and sines once, in fp64 (the angle in half turns, so that
-// its reduction is exact), and each warp norms and rotates the heads' rows, several
-// in flight.  Bound by memory.  VEC: rows are 16-byte aligned and a lane holds P
-// consecutive pairs; otherwise pairs lane, lane + 32, ...
-constexpr int kRopeTokens = 4, kRopeWarps = 8;
+// A warp takes a token and some of its heads' rows: a lane forms the cosines and sines
+// of its P pairs once for them, in fp64 (the angle in half turns, so that its
+// reduction is exact), then norms and rotates the rows, several in flight.  Bound by
+// memory.  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
+// otherwise pairs lane, lane + 32, ...
+constexpr int kRopeWarps = 8;
+__host__ __device__ constexpr int rope_ctas(int P) { return P < 4 ? 4 : 3; }  // per SM, 64 and 80 registers
 template <int P, bool HALVES, bool VEC>
-__global__ void __launch_bounds__(kRopeWarps * 32)
+__global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
     qk_norm_rope_kernel(const float* q, const float* k, float* q_out, float* k_out, int64_t qs, int64_t ks,
                         const float* __restrict__ wq, const float* __restrict__ wk, const int* __restrict__ positions,
-                        int n_tokens, int Hq, int Hkv, int D, int R, double log2_hi, double log2_lo, float eps) {
-  // A row's elements as D / 2 pairs: the R / 2 that rotate, then neighbours.  A lane's pairs:
-  constexpr int U = VEC ? 4 : 2;  // rows in flight
-  __shared__ float2 turn[kRopeTokens][32 * P];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = Hq + Hkv, half = R / 2;
+                        int n_tokens, int Hq, int Hkv, int D, int R, double log2_hi, double log2_lo, float eps,
+                        int rows, int shares) {
+  // A row's elements are D / 2 pairs: the R / 2 that rotate, then neighbours.
+  constexpr int U = VEC && P < 4 ? 4 : 2;  // rows in flight
+  const int lane = threadIdx.x & 31, heads = Hq + Hkv, half = R / 2;
   auto pair = [&](int i) { return VEC ? lane * P + i : lane + 32 * i; };
   auto first = [&](int p) { return HALVES && p < half ? p : 2 * p; };
   auto second = [&](int p) { return HALVES && p < half ? p + half : 2 * p + 1; };
-  const int my_pair = threadIdx.x % (32 * P), my_token = threadIdx.x / (32 * P);
-  const double f = my_pair < half ? rope_frequency(my_pair, R, log2_hi, log2_lo) * 0.31830988618379067154 : 0.0;
+  double f[P];
   float w[2][P][2];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int p = pair(i);
+    f[i] = p < half ? rope_frequency(p, R, log2_hi, log2_lo) * 0.31830988618379067154 : 0.0;
     const bool on = 2 * p < D;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -260,30 +277,21 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
       w[x][i][1] = on && wt ? __ldg(wt + second(p)) : 1.f;
     }
   }
-  for (int64_t tile = blockIdx.x; tile * kRopeTokens < n_tokens; tile += gridDim.x) {
-    const int n0 = (int)(tile * kRopeTokens), tokens = min(kRopeTokens, n_tokens - n0), rows = tokens * heads;
-    __syncthreads();
-    for (int n = my_token; n < tokens; n += kRopeWarps / P) {
-      double s, c;
-      sincospi(f * __ldg(positions + n0 + n), &s, &c);
-      turn[n][my_pair] = make_float2((float)c, (float)s);
-    }
-    __syncthreads();
-    for (int r0 = (blockIdx.y * kRopeWarps + warp) * U; r0 < rows; r0 += gridDim.y * kRopeWarps * U) {
-      float x[U][P][2];
-      int64_t at[U];
-      int token[U];
-      bool is_q[U], live[U];
+  const int64_t units = (int64_t)n_tokens * shares;
+  for (int64_t unit = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); unit < units;
+       unit += (int64_t)gridDim.x * kRopeWarps) {
+    const int n = (int)(unit / shares), share = (int)(unit - (int64_t)n * shares);
+    const int pos = __ldg(positions + n), h1 = min(heads, (share + 1) * rows);
+    int h0 = share * rows;
+    if (pos < 0) continue;
+    float x[U][P][2];
+    auto load = [&]() {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = r0 + u;
-        token[u] = min(r, rows - 1) / heads;
-        const int h = min(r, rows - 1) - token[u] * heads, n = n0 + token[u];
-        is_q[u] = h < Hq;
-        at[u] = is_q[u] ? n * qs + (int64_t)h * D : n * ks + (int64_t)(h - Hq) * D;
-        live[u] = r < rows && __ldg(positions + n) >= 0;
-        const float* in = (is_q[u] ? q : k) + at[u];
-        if (!live[u]) continue;
+        const int h = h0 + u;
+        if (h >= h1) break;
+        const bool is_q = h < Hq;
+        const float* in = is_q ? q + n * qs + (int64_t)h * D : k + n * ks + (int64_t)(h - Hq) * D;
         if constexpr (VEC && HALVES) {
           if constexpr (P == 1) {
             x[u][0][0] = in[lane];
@@ -318,20 +326,32 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
           }
         }
       }
+    };
+    load();
+    float2 turn[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      double s, c;
+      sincospi(f[i] * pos, &s, &c);
+      turn[i] = make_float2((float)c, (float)s);
+    }
+    for (;;) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!live[u]) continue;  // (the same in the whole warp)
+        const int h = h0 + u;
+        if (h >= h1) break;  // (the same in the whole warp)
+        const bool is_q = h < Hq;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < P; ++i) ss = fmaf(x[u][i][0], x[u][i][0], fmaf(x[u][i][1], x[u][i][1], ss));
         const float norm = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
-        float* out = (is_q[u] ? q_out : k_out) + at[u];
+        float* out = is_q ? q_out + n * qs + (int64_t)h * D : k_out + n * ks + (int64_t)(h - Hq) * D;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int p = pair(i);
-          const float a = x[u][i][0] * norm * (is_q[u] ? w[0][i][0] : w[1][i][0]);
-          const float b = x[u][i][1] * norm * (is_q[u] ? w[0][i][1] : w[1][i][1]);
-          const float2 t = p < half ? turn[token[u]][p] : make_float2(1.f, 0.f);
+          const float a = x[u][i][0] * norm * (is_q ? w[0][i][0] : w[1][i][0]);
+          const float b = x[u][i][1] * norm * (is_q ? w[0][i][1] : w[1][i][1]);
+          const float2 t = turn[i];
           x[u][i][0] = a * t.x - b * t.y;
           x[u][i][1] = a * t.y + b * t.x;
           if (p >= half) {  // only normed: as it is, infinities too
@@ -370,6 +390,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
           }
         }
       }
+      h0 += U;
+      if (h0 >= h1) break;
+      load();
     }
   }
 }
