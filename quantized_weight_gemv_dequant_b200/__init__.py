@@ -148,10 +148,11 @@ def lib():
 def _p(x):
     if x is None:
         return None
+    get = getattr(x, "data_ptr", None)  # a tensor, the argument of nearly every call
+    if get is not None:
+        return get()
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, ctypes.c_void_p):
         return x.value
     raise TypeError(f"cannot take a pointer from {type(x).__name__}")
@@ -254,9 +255,11 @@ def ntx_swiglu(gate, up, out, n, stream=None):
 def make_paged_kv(type, n_kv_heads, head_dim, page_size, n_pages, k_pages, v_pages, page_table, n_seqs,
                   max_pages) -> ntx_paged_kv:
     """The cache a paged call works on: pools of ntx_paged_kv_bytes(...) bytes each and a device int32
-    [n_seqs][max_pages] table.  The caller keeps the three buffers alive while calls use them."""
-    return ntx_paged_kv(type, n_kv_heads, head_dim, page_size, n_pages, n_seqs, max_pages, _p(k_pages), _p(v_pages),
-                        _p(page_table))
+    [n_seqs][max_pages] table.  Tensors among the three are kept alive with the returned object."""
+    kv = ntx_paged_kv(type, n_kv_heads, head_dim, page_size, n_pages, n_seqs, max_pages, _p(k_pages), _p(v_pages),
+                      _p(page_table))
+    kv.buffers = (k_pages, v_pages, page_table)
+    return kv
 
 
 def ntx_paged_kv_bytes(type, n_kv_heads, head_dim, page_size, n_pages) -> int:

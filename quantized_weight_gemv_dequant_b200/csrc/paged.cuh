@@ -517,12 +517,17 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x) {
                          bits_h2(0xD480D480u)));  // (1024 + 16 q) / 16 - 72
 }
 
-// Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.
+// Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.  A chunk is
+// 2 to 8 KiB of keys: 64 positions of the narrow rows (4-bit rows of 128: 131071
+// positions in 49 us, 52 with 32), 16 of fp16 rows of 256.  The CTAs are those whose
+// registers need no spills to speak of: 12 warps of Q8_0 at 168 registers read the
+// ragged batch of 64 sequences in 39 us, 16 at 128 in 42.
 template <int T, int D, int NC>
 struct PagedCfg {
-  static constexpr int CH = (T == kKvF16 && D == 256) ? 16 : 32;
-  static constexpr int SLOTS = (T == kKvF16 || (T == kKvQ8 && D >= 128)) ? 3 : 4;
-  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : D * NC <= 256 ? 3 : 2;
+  static constexpr int ROW = kv_row_bytes<T>(D);
+  static constexpr int CH = ROW <= 72 && D * NC <= 128 ? 64 : ROW <= 272 ? 32 : 16;
+  static constexpr int SLOTS = 3;
+  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : NC <= 2 ? 3 : 2;
   static constexpr int HEADS = 4 * NC;                     // query heads of a tile
   static constexpr int WARPS = 4;
   static constexpr int CB = kv_code_bytes<T>(D);           // bytes of a row's codes
@@ -584,15 +589,15 @@ struct PagedParts {
   PagedParts() = default;
   __device__ __forceinline__ PagedParts(int64_t W, int warps) : n((int)min64(W, warps)), size(0), longer(0) {
     if (n == 0) return;
-    size = W >> 31 ? W / n : (int)W / n;
+    size = W >> 31 ? W / n : (int)W / n;  // (64-bit divisions only where they are needed)
     longer = W - size * n;
   }
   __device__ __forceinline__ int64_t begin(int w) const { return w * size + min64(w, longer); }
   __device__ __forceinline__ int holder(int64_t unit) const {  // the part of a unit
     const int64_t head = longer * (size + 1);
-    if (unit < head) return (int)(unit >> 31 ? unit / (size + 1) : (int)unit / (int)(size + 1));
+    if (unit < head) return (int)((unit | size) >> 30 ? unit / (size + 1) : (int)unit / (int)(size + 1));
     unit -= head;
-    return (int)(longer + (unit >> 31 ? unit / size : (int)unit / (int)size));
+    return (int)(longer + ((unit | size) >> 30 ? unit / size : (int)unit / (int)size));
   }
 };
 // Units of each of a sequence's items.
@@ -724,8 +729,8 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
           ld_rows[r] = rows;
           ld_at[r] = ((int64_t)page * c.n_kv_heads + ld.kvh) * head_bytes + lane_off;
         }
-        const uint8_t* codes = pool + ld_at[r] + ld_first[r] * F::CB;
-        const uint8_t* sc = pool + ld_at[r] + (scales_at + ld_first[r] * F::SB);
+        const uint8_t* codes = pool + ld_at[r] + (int64_t)ld_first[r] * F::CB;
+        const uint8_t* sc = pool + ld_at[r] + (scales_at + (int64_t)ld_first[r] * F::SB);
         const uint32_t dst = ld_slot + 16 * r * F::CB + (V ? lane_v : lane_k);
         const uint32_t dst_sc = ld_slot + CH * F::CB + r * 16 * F::SB + lane_off;
         auto place = [&](int i) {
@@ -769,11 +774,7 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
   constexpr std::true_type kV{};
   load(kK);
   load(kV);
-  if constexpr (F::SLOTS == 4) load(kK);
-  // what is loaded while K / V of a chunk is used: SLOTS - 1 slots ahead
-  constexpr std::bool_constant<F::SLOTS == 4> with_k{};
-  constexpr std::bool_constant<F::SLOTS == 3> with_v{};
-  static_assert(F::SLOTS == 3 || F::SLOTS == 4);
+  static_assert(F::SLOTS == 3);  // while K (V) of a chunk is used, K (V) of the next is loaded
 
   // scales of a row, two blocks a word
   auto scales = [&](uint32_t row, uint32_t sc[NB / 2]) {
@@ -791,22 +792,23 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
 
   // p is kept 2^kPBits fold, in l and o too
   constexpr float kPBits = T == kKvF16 ? 14.f : 10.f;
-  // Block types' keys enter the products as fp16 subnormals, (code + offset) 2^-24
-  constexpr float kCodeUnit = T == kKvF16 ? 1.f : 16777216.f;
+  // Block types' keys enter the products as fp16 subnormals, (code + 128) 2^-24 or (code + 8) 2^-20: an instruction
+  // for two elements, no conversion.  The offset's share of a block's product is known with q and taken off in
+  // fp32.  (The instruction aligns its products by the operands' exponents, and a subnormal's is 2^-14: nibbles as
+  // 2^-24 would lie so far below that the output is off by 1e-6, instead of 4e-7.  Converted to normal numbers,
+  // 131071 positions of Q4_0 take 54 us instead of 49.  Not for values: all weights have one sign, and the
+  // offset's share would grow faster than the sum.)
+  constexpr float kCodeUnit = T == kKvQ8 ? 16777216.f : T == kKvQ4 ? 1048576.f : 1.f;
   // This lane's heads: t of column tile c as a softmax row (with positions g, g + 8 of 16)
   // and in o (with two elements of 16); g / 2 in q's fragments.
   uint32_t qf[NC][NB][4];
   float o[NC][NT][2], m[NC], l[NC], to_log2[NC];
-  float off[NC][NB];  // block types: the offset's share of a block's product
+  float off[NC][NB];  // block types: minus the offset's share of a block's product
   bool fresh = true;
   int rows = 0, head0 = 0;
 
   for (;;) {
-    // ---- scores
-    cp_async_wait<F::SLOTS - 2>();
-    __syncwarp();
-    load(with_k);
-    if (fresh) {
+    if (fresh) {  // ---- an item's q, while its first keys are on the way
       rows = min(F::HEADS, G - F::HEADS * cur.rt);
       head0 = cur.kvh * G + F::HEADS * cur.rt;
 #pragma unroll
@@ -839,21 +841,19 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // the pairs that a key fragment of this type has: elements 0 1, 2 3, ... or 0 2, 1 3, ... of
-            // this lane's; a high nibble counts 16 fold
+            // the pairs that a key fragment of this type has: elements 0 1, 2 3, ... or 0 2, 1 3, ... of this lane's
             const int i0 = T == kKvQ4 ? 4 * (i >> 1) + (i & 1) : 2 * i, i1 = T == kKvQ4 ? i0 + 2 : i0 + 1;
-            const float w = T == kKvQ4 && i >= 2 ? 0.0625f : 1.f;
             uint32_t hi, lo;
-            split2(x[b][i0] * up * w, x[b][i1] * up * w, hi, lo);
+            split2(x[b][i0] * up, x[b][i1] * up, hi, lo);
             qf[ct][b][i] = (g & 1) ? lo : hi;
             const float2 f = __half22float2(bits_h2(qf[ct][b][i]));
-            sum = fmaf(f.x + f.y, 1.f / w, sum);
+            sum += f.x + f.y;
           }
           if constexpr (T != kKvF16) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             sum = __shfl_sync(0xffffffffu, sum, 8 * t) + __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-            off[ct][b] = sum * (-(T == kKvQ4 ? 8.f : 128.f) / kCodeUnit);
+            off[ct][b] = sum * (-(T == kKvQ8 ? 128.f : 8.f) / kCodeUnit);
           }
         }
 #pragma unroll
@@ -863,6 +863,11 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
       }
       fresh = false;
     }
+
+    // ---- scores
+    cp_async_wait<F::SLOTS - 2>();
+    __syncwarp();
+    load(kK);
 
     float s[NC][NS][2];
     if constexpr (T == kKvF16) {
@@ -909,9 +914,10 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
             a1[2] = __byte_perm(u.y, 0, 0x4342); a1[3] = __byte_perm(v.y, 0, 0x4342);
           } else {
             const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, b) * 16 + 4 * t;
-            const uint32_t u = lds32(a), v = lds32(a + 8 * F::CB), u8 = u >> 8, v8 = v >> 8;
-            a0[0] = u & 0x000F000Fu; a0[1] = v & 0x000F000Fu; a0[2] = u8 & 0x000F000Fu; a0[3] = v8 & 0x000F000Fu;
-            a1[0] = u & 0x00F000F0u; a1[1] = v & 0x00F000F0u; a1[2] = u8 & 0x00F000F0u; a1[3] = v8 & 0x00F000F0u;
+            constexpr uint32_t M = 0x00F000F0u;  // every nibble 16 fold
+            const uint32_t u = lds32(a), v = lds32(a + 8 * F::CB);
+            a0[0] = (u << 4) & M; a0[1] = (v << 4) & M; a0[2] = (u >> 4) & M; a0[3] = (v >> 4) & M;
+            a1[0] = u & M; a1[1] = v & M; a1[2] = (u >> 8) & M; a1[3] = (v >> 8) & M;
           }
           float d[2];
 #pragma unroll
@@ -942,9 +948,18 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           s[ct][k][i] *= to_log2[ct];
-          if (left < CH && 16 * k + 8 * i + g >= left) s[ct][k][i] = -INFINITY;  // behind the sequence
           top = fmaxf(top, s[ct][k][i]);
         }
+      if (left < CH) {  // behind the sequence
+        top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (16 * k + 8 * i + g >= left) s[ct][k][i] = -INFINITY;
+            top = fmaxf(top, s[ct][k][i]);
+          }
+      }
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float m_new = fmaxf(m[ct], top), zero = m_new == -INFINITY ? 0.f : m_new, base = zero - kPBits;
@@ -970,7 +985,7 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     // ---- weighted values
     cp_async_wait<F::SLOTS - 2>();
     __syncwarp();
-    load(with_v);
+    load(kV);
     if constexpr (T == kKvF16) {
       uint32_t p[NC][NS][2];
 #pragma unroll

@@ -802,3 +802,94 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for m, m2 in pairs:
         assert torch.equal(m.out, m2.out)
+
+
+# ------------------------------------------------------------------ large caches, first calls
+@pytest.mark.parametrize("kind,d,ps", [(F16, 256, 2 ** 23 + 16), (Q8, 256, 2 ** 24 + 16), (Q4, 256, 2 ** 25 + 16)])
+def test_one_page_longer_than_4_gib(kind, d, ps):
+    """A contiguous cache whose rows and scales lie past 32-bit byte offsets.  Keys are zero, so all weights are
+    1 / n; values are zero but for rows at the far end, in the middle and at the front.  The sum of n equal weights
+    and of the values is exact to 1e-5 relative (every partial sum of the weights is a multiple of 2^-24 of it)."""
+    torch = _t()
+    size = ntx.ntx_paged_kv_bytes(kind, 1, d, ps, 1)
+    assert size > 2 ** 32
+    pools = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    kv = ntx.make_paged_kv(kind, 1, d, ps, 1, *pools, torch.zeros(1, dtype=torch.int32, device="cuda"), 1, 1)
+    n = ps - 3
+    pos = torch.tensor([n - 1, ps // 2 + 5, 0, n - 40], dtype=torch.int32, device="cuda")
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+    v = torch.from_numpy(sg.fill_f32(181, "v", 4 * d).reshape(4, d)).cuda()
+    ntx.ntx_kv_append(kv, torch.zeros_like(v), v, d, d, ids, pos, 4)
+    back = torch.zeros(2, 4, d, device="cuda")
+    ntx.ntx_kv_read(kv, back[0], back[1], d, d, ids, pos, 4)
+    h = v.cpu().numpy()
+    codes, scales = blocks_of(kind, h)
+    want = values_of(kind, codes, scales)
+    assert torch.all(back[0] == 0) and np.array_equal(back[1].cpu().numpy(), want.astype(np.float32))
+    # rows of a zeroed Q4_0 pool hold code 0, -8 times the scale 0
+    ws_n = ntx.ntx_attn_paged_workspace_bytes(kv, 2)
+    ws, out = torch.empty(ws_n, dtype=torch.uint8, device="cuda"), torch.empty(2, d, device="cuda")
+    q = torch.from_numpy(sg.fill_f32(181, "q", 2 * d)).cuda()
+    ntx.ntx_attn_decode_paged(kv, q, 2 * d, out, 2, torch.tensor([n], dtype=torch.int32, device="cuda"), 0.0625, ws, ws_n)
+    got = out.cpu().numpy().astype(np.float64)
+    mean = want.sum(0) / n
+    assert np.all(np.abs(got - mean) <= 1e-5 * np.abs(want).sum(0) / n)
+    del pools, kv
+    torch.cuda.empty_cache()
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import quantized_weight_gemv_dequant_b200 as ntx
+hkv, hq, d, ps = 2, 8, 128, 16
+pools = [torch.zeros(ntx.ntx_paged_kv_bytes(ntx.NTX_Q8_0, hkv, d, ps, 4), dtype=torch.uint8, device="cuda") for _ in range(2)]
+kv = ntx.make_paged_kv(ntx.NTX_Q8_0, hkv, d, ps, 4, *pools, torch.arange(4, dtype=torch.int32, device="cuda"), 1, 4)
+x = torch.randn((hq + 2 * hkv) * d, device="cuda")
+pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+n = torch.ones(1, dtype=torch.int32, device="cuda")
+ws_n = ntx.ntx_attn_paged_workspace_bytes(kv, hq)
+ws, out = torch.zeros(ws_n, dtype=torch.uint8, device="cuda"), torch.zeros(hq, d, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s = torch.cuda.current_stream()
+    k, v = x[hq * d:], x[(hq + hkv) * d:]
+    ntx.ntx_qk_norm_rope(x, k, x, k, hq * d, hkv * d, None, None, pos, 1, hq, hkv, d, d, 1, 1e4, 1e-6, s)
+    ntx.ntx_kv_append(kv, k, v, hkv * d, hkv * d, None, pos, 1, s)
+    ntx.ntx_attn_decode_paged(kv, x, hq * d, out, hq, n, 0.1, ws, ws_n, s)
+g.replay()
+torch.cuda.synchronize()
+want = torch.zeros(hkv, d, device="cuda")
+ntx.ntx_kv_read(kv, None, want, 0, hkv * d, None, pos, 1)
+assert torch.allclose(out, want.repeat_interleave(hq // hkv, 0), rtol=1e-6, atol=0)
+assert ntx.ntx_device_status() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE.format(root=root)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
+
+
+def test_attention_workspace_is_enough_and_no_more_is_touched():
+    """Guard bytes behind the workspace of every kernel variant stay, at lengths that split every item."""
+    torch = _t()
+    for kind in TYPES:
+        for d in (64, 128, 256):
+            for hq, hkv in ((2, 2), (12, 2), (16, 1), (40, 1)):
+                c = Cache(kind, hkv, d, 16, [3000, 700], 191)
+                for p in c.pools:
+                    p.zero_()
+                n = ntx.ntx_attn_paged_workspace_bytes(c.kv, hq)
+                ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+                q = torch.ones(2, hq, d, device="cuda")
+                out = attend(c, q, [3000, 700], hq, 0.1, ws=ws[:n])
+                assert torch.all(ws[n:] == 0x5A) and torch.all(out == 0)
