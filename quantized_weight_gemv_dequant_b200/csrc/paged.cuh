@@ -49,6 +49,28 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
 constexpr int kTokenWarps = 4;  // tokens of a CTA
 
+// Where a lane's four elements of step i of a piece lie: a step is 128 elements, 128 / D
+// heads or a half of one.
+template <int T, int D>
+struct PieceAt {
+  uint8_t *codes, *scales;  // step 0's
+  int64_t head_bytes;
+  __device__ __forceinline__ PieceAt(const ntx_paged_kv& c, void* pool, int64_t page, int row, int e0) {
+    head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D);
+    const int e = e0 % D, blk = e / 32, sub = e % 32 / 4;
+    uint8_t* part = static_cast<uint8_t*>(pool) + (page * c.n_kv_heads + e0 / D) * head_bytes;
+    codes = part + (int64_t)row * kv_code_bytes<T>(D) +
+            (T == kKvF16 ? 2 * e : T == kKvQ8 ? e : blk * 16 + (sub & 3) * 4);
+    scales = part + (int64_t)c.page_size * kv_code_bytes<T>(D) + row * (D / 16ll) + blk * 2;
+  }
+  __device__ __forceinline__ uint8_t* code(int i) const {
+    return codes + i * 128 / D * head_bytes + kv_code_bytes<T>(i * 128 % D);
+  }
+  __device__ __forceinline__ uint16_t* scale(int i) const {
+    return reinterpret_cast<uint16_t*>(scales + i * 128 / D * head_bytes + i * 128 % D / 16);
+  }
+};
+
 // ------------------------------------------------------------- cache write
 // A code is the fp32 quotient w / d rounded half away from zero.  w times rcp(d),
 // within 2^-14 of the quotient (which is at most 127, or 8), tells it unless it is
@@ -93,7 +115,6 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
                                                                      int64_t vs, const int* __restrict__ seq_ids,
                                                                      const int* __restrict__ positions, int n_tokens,
                                                                      bool vec, int pieces, int* status) {
-  constexpr int nb = D / 32;
   const int width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
   const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
   if (n >= n_tokens) return;
@@ -119,21 +140,18 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
   int64_t page;
   int row;
   if (pos < 0 || !kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) return;
-  uint8_t* part0 = static_cast<uint8_t*>(is_v ? c.v_pages : c.k_pages) +
-                   page * c.n_kv_heads * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+  const PieceAt<T, D> at(c, is_v ? c.v_pages : c.k_pages, page, row, e0);
 #pragma unroll
   for (int i = 0; i < kPieceSteps; ++i) {
     const int e = e0 + i * 128;
     if (e - lane * 4 >= width) break;
     const bool on = e < width;
-    const int head = e / D, blk = (e - head * D) >> 5;
-    uint8_t* part = part0 + head * ((int64_t)c.page_size * kv_row_bytes<T>(D));
     if constexpr (T == kKvF16) {
       if (on) {
         uint2 h;
         h.x = float_to_half_bits(w[i][0]) | ((uint32_t)float_to_half_bits(w[i][1]) << 16);
         h.y = float_to_half_bits(w[i][2]) | ((uint32_t)float_to_half_bits(w[i][3]) << 16);
-        *reinterpret_cast<uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2) = h;
+        *reinterpret_cast<uint2*>(at.code(i)) = h;
       }
     } else {
       float top = max_nan(max_nan(fabsf(w[i][0]), fabsf(w[i][1])), max_nan(fabsf(w[i][2]), fabsf(w[i][3])));
@@ -160,15 +178,12 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
       // zeros and blocks that are not finite: codes of zero
       const uint32_t codes = top > 0.f && finite ? quotient_codes<T>(w[i], d) : T == kKvQ8 ? 0u : 0x08080808u;
       if constexpr (T == kKvQ8) {
-        if (on) *reinterpret_cast<uint32_t*>(part + (int64_t)row * D + blk * 32 + sub * 4) = codes;
+        if (on) *reinterpret_cast<uint32_t*>(at.code(i)) = codes;
       } else {
         const uint32_t hi = __shfl_down_sync(0xffffffffu, codes, 4, 8);  // elements 16 further on
-        if (on && sub < 4)
-          *reinterpret_cast<uint32_t*>(part + (int64_t)row * (D / 2) + blk * 16 + sub * 4) = codes | (hi << 4);
+        if (on && sub < 4) *reinterpret_cast<uint32_t*>(at.code(i)) = codes | (hi << 4);
       }
-      if (on && sub == 0)
-        *reinterpret_cast<uint16_t*>(part + (int64_t)c.page_size * kv_code_bytes<T>(D) + ((int64_t)row * nb + blk) * 2) =
-            finite ? float_to_half_bits(d) : (uint16_t)0x7FFF;
+      if (on && sub == 0) *at.scale(i) = finite ? float_to_half_bits(d) : (uint16_t)0x7FFF;
     }
   }
 }
@@ -180,7 +195,6 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_pag
                                                                    const int* __restrict__ seq_ids,
                                                                    const int* __restrict__ positions, int n_tokens,
                                                                    bool vec, int pieces, int* status) {
-  constexpr int nb = D / 32;
   const int width = c.n_kv_heads * D, lane = threadIdx.x & 31, sub = lane & 7;
   const int n = blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
   if (n >= n_tokens) return;
@@ -192,23 +206,18 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_pag
   int64_t page;
   int row;
   if (pos < 0 || !kv_place(c, seq_ids ? __ldg(seq_ids + n) : n, pos, &page, &row, status)) return;
-  const uint8_t* part0 = static_cast<const uint8_t*>(is_v ? c.v_pages : c.k_pages) +
-                         page * c.n_kv_heads * ((int64_t)c.page_size * kv_row_bytes<T>(D));
+  const PieceAt<T, D> at(c, is_v ? c.v_pages : c.k_pages, page, row, e0);
   uint2 code[kPieceSteps];
   uint16_t scale[kPieceSteps];
 #pragma unroll
   for (int i = 0; i < kPieceSteps; ++i) {
     const int e = e0 + i * 128;
     if (e >= width) break;
-    const int head = e / D, blk = (e - head * D) >> 5;
-    const uint8_t* part = part0 + head * ((int64_t)c.page_size * kv_row_bytes<T>(D));
     if constexpr (T == kKvF16) {
-      code[i] = __ldcs(reinterpret_cast<const uint2*>(part + ((int64_t)row * D + blk * 32 + sub * 4) * 2));
+      code[i] = *reinterpret_cast<const uint2*>(at.code(i));
     } else {
-      const int at = T == kKvQ8 ? blk * 32 + sub * 4 : blk * 16 + (sub & 3) * 4;
-      code[i].x = *reinterpret_cast<const uint32_t*>(part + (int64_t)row * kv_code_bytes<T>(D) + at);
-      scale[i] = *reinterpret_cast<const uint16_t*>(part + (int64_t)c.page_size * kv_code_bytes<T>(D) +
-                                                    ((int64_t)row * nb + blk) * 2);
+      code[i].x = *reinterpret_cast<const uint32_t*>(at.code(i));
+      scale[i] = *at.scale(i);
     }
   }
 #pragma unroll
