@@ -95,17 +95,20 @@ __device__ __forceinline__ uint32_t quotient_codes(const float w[4], float d) {
   for (int i = 0; i < 4; ++i) {
     const float x = w[i] * r, y = x + kMagic;
     sure &= fabsf(x - (y - kMagic)) < 0.5f - 0x1p-14f;
-    m[i] = __float_as_uint(T == kKvQ4 ? fminf(y, kMagic + 7.f) : y);
+    m[i] = __float_as_uint(y);
   }
-  if (sure) return __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+  if (sure) {
+    const uint32_t c = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+    return T == kKvQ4 ? c - (c >> 4 & 0x01010101u) : c;  // 16, the largest's opposite, is 15
+  }
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) codes |= quotient_code<T>(w[i], d) << (8 * i);
   return codes;
 }
-__device__ __forceinline__ float max_nan(float x, float y) {  // NaN if either is
+__device__ __forceinline__ float max_nan(float x, float y, float z) {  // NaN if any is
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 
@@ -154,9 +157,9 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
         *reinterpret_cast<uint2*>(at.code(i)) = h;
       }
     } else {
-      float top = max_nan(max_nan(fabsf(w[i][0]), fabsf(w[i][1])), max_nan(fabsf(w[i][2]), fabsf(w[i][3])));
+      float top = max_nan(max_nan(fabsf(w[i][0]), fabsf(w[i][1]), fabsf(w[i][2])), fabsf(w[i][3]), 0.f);
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
       const bool finite = top < INFINITY;
       float d;
       if constexpr (T == kKvQ8) {
