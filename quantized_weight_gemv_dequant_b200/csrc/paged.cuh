@@ -827,21 +827,25 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
       for (int ct = 0; ct < NC; ++ct) {
         const int h = 4 * ct + (g >> 1);
         const float* qp = q + cur.s * qs + (int64_t)(head0 + h) * D;
-        float x[NB][8], top = 0.f;
+        // The two lanes of a head's columns (one keeps the upper parts, one the remainders) form every other block
+        // each, and exchange.
+        const int odd = g & 1;
+        float x[NB / 2][8], top = 0.f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int i = 0; i < NB / 2; ++i) {
+          const float* p = qp + 32 * (2 * i + odd);
           float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
           if (h < rows) {
-            u = ldg4(qp + 32 * b + (T == kKvQ4 ? 4 * t : 8 * t));
-            v = ldg4(qp + 32 * b + (T == kKvQ4 ? 16 + 4 * t : 8 * t + 4));
+            u = ldg4(p + (T == kKvQ4 ? 4 * t : 8 * t));
+            v = ldg4(p + (T == kKvQ4 ? 16 + 4 * t : 8 * t + 4));
           }
-          x[b][0] = u.x; x[b][1] = u.y; x[b][2] = u.z; x[b][3] = u.w;
-          x[b][4] = v.x; x[b][5] = v.y; x[b][6] = v.z; x[b][7] = v.w;
+          x[i][0] = u.x; x[i][1] = u.y; x[i][2] = u.z; x[i][3] = u.w;
+          x[i][4] = v.x; x[i][5] = v.y; x[i][6] = v.z; x[i][7] = v.w;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i][j]));
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int y = 1; y < 8; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
         // 2^e with top 2^e in [2^13, 2^14), as far as fp32 has it; 1 for infinities
         const int eb = __float_as_int(top) >> 23;
         const int es = eb == 255 ? 127 : min(254, 267 - eb);
@@ -849,23 +853,28 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
         const float down = es == 254 ? __int_as_float(0x00400000) : __int_as_float((254 - es) << 23);
         to_log2[ct] = __shfl_sync(0xffffffffu, scale * down * (1.44269504088896340736f * kCodeUnit), 8 * t);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int i = 0; i < NB / 2; ++i) {
           float sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int j = 0; j < 4; ++j) {
             // the pairs that a key fragment of this type has: elements 0 1, 2 3, ... or 0 2, 1 3, ... of this lane's
-            const int i0 = T == kKvQ4 ? 4 * (i >> 1) + (i & 1) : 2 * i, i1 = T == kKvQ4 ? i0 + 2 : i0 + 1;
+            const int j0 = T == kKvQ4 ? 4 * (j >> 1) + (j & 1) : 2 * j, j1 = T == kKvQ4 ? j0 + 2 : j0 + 1;
             uint32_t hi, lo;
-            split2(x[b][i0] * up, x[b][i1] * up, hi, lo);
-            qf[ct][b][i] = (g & 1) ? lo : hi;
-            const float2 f = __half22float2(bits_h2(qf[ct][b][i]));
-            sum += f.x + f.y;
+            split2(x[i][j0] * up, x[i][j1] * up, hi, lo);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? hi : lo, 4);
+            qf[ct][2 * i][j] = odd ? other : hi;
+            qf[ct][2 * i + 1][j] = odd ? lo : other;
+            if constexpr (T != kKvF16) {
+              const float2 f = __half22float2(bits_h2(hi)), r = __half22float2(bits_h2(lo));
+              sum += (f.x + f.y) + (r.x + r.y);
+            }
           }
           if constexpr (T != kKvF16) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum = __shfl_sync(0xffffffffu, sum, 8 * t) + __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-            off[ct][b] = sum * (-(T == kKvQ8 ? 128.f : 8.f) / kCodeUnit);
+            sum *= -(T == kKvQ8 ? 128.f : 8.f) / kCodeUnit;
+            off[ct][2 * i] = __shfl_sync(0xffffffffu, sum, 8 * t);
+            off[ct][2 * i + 1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
           }
         }
 #pragma unroll
