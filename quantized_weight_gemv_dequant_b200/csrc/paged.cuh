@@ -256,10 +256,21 @@ __device__ __forceinline__ double rope_frequency(int p, int R, double log2_hi, d
   return exp2(-q) * (1.0 - 0.69314718055994530942 * rest);
 }
 
+// Cosine and sine of t half turns: t less the nearest multiple of a quarter turn is
+// exact in fp64 and rounds to fp32 within 2^-27 of a half turn, 2e-8; sine and cosine
+// of at most an eighth of a turn are fp32's.
+__device__ __forceinline__ float2 rope_turn(double t) {
+  const double n = rint(2.0 * t);
+  float s, c;
+  sincospif((float)fma(-0.5, n, t), &s, &c);
+  const int k = (int)n;  // |t| < 2^31 / pi
+  const float x = (k & 1) ? s : c, y = (k & 1) ? c : s;
+  return make_float2(((k + 1) & 2) ? -x : x, (k & 2) ? -y : y);
+}
+
 // A warp takes a token and some of its heads' rows: a lane forms the cosines and sines
-// of its P pairs once for them, in fp64 (the angle in half turns, so that its
-// reduction is exact), then norms and rotates the rows, several in flight.  Bound by
-// memory.  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
+// of its P pairs once for them, then norms and rotates the rows, several in flight.
+// Bound by memory.  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
 // otherwise pairs lane, lane + 32, ...
 constexpr int kRopeWarps = 8;
 __host__ __device__ constexpr int rope_ctas(int P) { return P < 4 ? 4 : 3; }  // per SM, 64 and 80 registers
@@ -343,9 +354,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
     float2 turn[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      double s, c;
-      sincospi(f[i] * pos, &s, &c);
-      turn[i] = make_float2((float)c, (float)s);
+      turn[i] = rope_turn(f[i] * pos);
     }
     for (;;) {
 #pragma unroll
