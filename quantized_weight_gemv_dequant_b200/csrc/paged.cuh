@@ -256,6 +256,12 @@ __device__ __forceinline__ double rope_frequency(int p, int R, double log2_hi, d
   return exp2(-q) * (1.0 - 0.69314718055994530942 * rest);
 }
 
+// 1 / sqrt(x): the approximation (2^-22.4) and a step of Newton's, within 2^-23.
+__device__ __forceinline__ float rope_rsqrt(float x) {
+  const float r = rsqrtf(x), y = r * fmaf(-0.5f * x * r, r, 1.5f);
+  return x > 0.f && x < INFINITY ? y : r;
+}
+
 // Cosine and sine of t half turns: t less the nearest multiple of a quarter turn is
 // exact in fp64 and rounds to fp32 within 2^-27 of a half turn, 2e-8; sine and cosine
 // of at most an eighth of a turn are fp32's.
@@ -300,6 +306,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
       w[x][i][1] = on && wt ? __ldg(wt + second(p)) : 1.f;
     }
   }
+  const float inv_d = 1.0f / (float)D;
   const int64_t units = (int64_t)n_tokens * shares;
   for (int64_t unit = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); unit < units;
        unit += (int64_t)gridDim.x * kRopeWarps) {
@@ -307,6 +314,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
     const int pos = __ldg(positions + n), h1 = min(heads, (share + 1) * rows);
     int h0 = share * rows;
     if (pos < 0) continue;
+    const int64_t at_q = n * qs, at_k = n * ks - (int64_t)Hq * D;  // where head 0's row would be
     float x[U][P][2];
     auto load = [&]() {
 #pragma unroll
@@ -314,7 +322,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
         const int h = h0 + u;
         if (h >= h1) break;
         const bool is_q = h < Hq;
-        const float* in = is_q ? q + n * qs + (int64_t)h * D : k + n * ks + (int64_t)(h - Hq) * D;
+        const float* in = (is_q ? q + at_q : k + at_k) + h * D;
         if constexpr (VEC && HALVES) {
           if constexpr (P == 1) {
             x[u][0][0] = in[lane];
@@ -365,8 +373,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < P; ++i) ss = fmaf(x[u][i][0], x[u][i][0], fmaf(x[u][i][1], x[u][i][1], ss));
-        const float norm = 1.0f / sqrtf(warp_sum(ss) / (float)D + eps);
-        float* out = is_q ? q_out + n * qs + (int64_t)h * D : k_out + n * ks + (int64_t)(h - Hq) * D;
+        const float norm = rope_rsqrt(fmaf(warp_sum(ss), inv_d, eps));
+        float* out = (is_q ? q_out + at_q : k_out + at_k) + h * D;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const int p = pair(i);
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
           const float2 t = turn[i];
           x[u][i][0] = a * t.x - b * t.y;
           x[u][i][1] = a * t.y + b * t.x;
-          if (p >= half) {  // only normed: as it is, infinities too
+          if (!(VEC && HALVES) && p >= half) {  // only normed: as it is, infinities too
             x[u][i][0] = a;
             x[u][i][1] = b;
           }
