@@ -148,7 +148,7 @@ cudaError_t with_attn(const ntx_paged_kv* kv, int n_q_heads, F f) {
 size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
   size_t n = 0;
   with_attn(kv, n_q_heads, [&](auto t, auto d, auto nc) {
-    using F = PagedCfg<decltype(t)::value, decltype(d)::value, decltype(nc)::value>;
+    using F = PagedCfg<decltype(t)::value, decltype(d)::value, decltype(nc)::value, false>;
     const size_t warps = (size_t)sm_count() * F::CTAS * F::WARPS;
     const int G = n_q_heads / kv->n_kv_heads;
     n = warps * 2 * (sizeof(int4) + sizeof(float) * paged_part_floats(G < F::HEADS ? G : F::HEADS, kv->head_dim));
@@ -160,14 +160,25 @@ size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
 template <int T, int D, int NC>
 cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
                               const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
-  using F = PagedCfg<T, D, NC>;
+  using F = PagedCfg<T, D, NC, false>;
   static std::atomic<unsigned long long> done{0};
   const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS, G = Hq / kv.n_kv_heads;
+  using O = PagedCfg<T, D, NC, true>;
+  const int64_t items = (int64_t)kv.n_seqs * kv.n_kv_heads * ((G + O::HEADS - 1) / O::HEADS);
+  const int64_t ctx = (int64_t)kv.max_pages * kv.page_size;
+  if (items <= sm_count() && ctx <= (2 * items < sm_count() ? kOneCtaCtx : kOneCtaCtxMany)) {
+    static std::atomic<unsigned long long> done_one{0};
+    const cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done_one);
+    if (e != cudaSuccess) return e;
+    attn_paged_kernel<T, D, NC, true><<<(int)items, O::WARPS * 32, O::SMEM, stream>>>(
+        kv, q, qs, out, nullptr, nullptr, Hq, lens, scale, device_status_ptr());
+    return cudaGetLastError();
+  }
   int4* split = static_cast<int4*>(ws);
   float* part = reinterpret_cast<float*>(split + 2 * (size_t)warps);
-  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC>, F::SMEM, done);
+  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, false>, F::SMEM, done);
   if (e != cudaSuccess) return e;
-  attn_paged_kernel<T, D, NC><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, split, part, Hq, lens, scale,
+  attn_paged_kernel<T, D, NC, false><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, split, part, Hq, lens, scale,
                                                                        device_status_ptr());
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -44,8 +44,12 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 
 // A warp of the write and of the read handles one row's piece of kPiece elements,
 // four consecutive ones to a lane at a time (eight lanes a block of 32), all its
-// loads in flight at once.  Both kernels are bound by memory; a row's place is
-// looked up once a piece.
+// loads in flight at once; a row's place is looked up once a piece.  On B200, 24001
+// tokens of 8 heads of 128 from Q8_0: 44 us, 5.6 TB/s, 0.86 of a copy's bandwidth;
+// 16384 tokens to Q4_0 and back: 42 and 28 us, 3.6 and 5.4 TB/s.  The write to 4 bits
+// is bound by its 135 instructions for each 128 elements (ALU pipe at 0.66, issue at
+// 0.75), everything else by memory.  Pieces of 1024 elements are 3 % faster on long
+// prompts and 25 % slower on one token.
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
 constexpr int kTokenWarps = 4;  // tokens of a CTA
 
@@ -276,7 +280,10 @@ __device__ __forceinline__ float2 rope_turn(double t) {
 
 // A warp takes a token and some of its heads' rows: a lane forms the cosines and sines
 // of its P pairs once for them, then norms and rotates the rows, several in flight.
-// Bound by memory.  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
+// Bound by memory: 8192 tokens of 72 heads of 128 take 101 us, 6.0 TB/s, 0.92 of a
+// copy's bandwidth (angles shared by a CTA through shared memory: 117 us; sines and
+// cosines in fp64: 110; a tile's next rows loaded ahead: 138, the registers cost a
+// CTA).  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
 // otherwise pairs lane, lane + 32, ...
 constexpr int kRopeWarps = 8;
 __host__ __device__ constexpr int rope_ctas(int P) { return P < 4 ? 4 : 3; }  // per SM, 64 and 80 registers
@@ -457,7 +464,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
 // Warps share nothing: each streams K and V chunks through its own ring of
 // shared-memory slots with 16-byte asynchronous copies, across items, without a
 // barrier.  The order of every sum is fixed by lengths and grid.
-
+//
+// Why not the fifth-generation tensor cores: the work is bound by memory (F16) or by
+// taking codes apart (block types), not by products (hmma pipe at 0.10 to 0.16), and
+// their operands would have to pass through shared memory once more.
+//
+// Measured on B200, 32 query heads over 8 KV heads of 128, with the join: one fp16
+// sequence of 131071 positions 88 us (6.1 TB/s, 0.93 of a copy's bandwidth; without
+// the join 84); Q8_0 53 us (0.82), Q4_0 49 us (0.47: 870 instructions a chunk of 32
+// positions, issue at 0.63); 64 sequences of 1 to 8191 positions in Q8_0 38.5 us
+// (0.72).  Before items' starts counted as work the longest-running SM of that batch
+// took 80 k cycles where the others took 64 k.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -546,26 +563,28 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x) {
                          bits_h2(0xD480D480u)));  // (1024 + 16 q) / 16 - 72
 }
 
+constexpr int kMaxTile = 16;  // heads of a tile at most: a part is (m, l)[16], o[heads][D]
+__host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * kMaxTile; }
+
 // Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.  A chunk is
 // 2 to 8 KiB of keys: 64 positions of the narrow rows (4-bit rows of 128: 131071
 // positions in 49 us, 52 with 32), 16 of fp16 rows of 256.  The CTAs are those whose
 // registers need no spills to speak of: 12 warps of Q8_0 at 168 registers read the
 // ragged batch of 64 sequences in 39 us, 16 at 128 in 42.
-template <int T, int D, int NC>
+template <int T, int D, int NC, bool ONE>
 struct PagedCfg {
   static constexpr int ROW = kv_row_bytes<T>(D);
   static constexpr int CH = ROW <= 72 && D * NC <= 128 ? 64 : ROW <= 272 ? 32 : 16;
   static constexpr int SLOTS = 3;
-  static constexpr int CTAS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : NC <= 2 ? 3 : 2;
+  static constexpr int FOURS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : NC <= 2 ? 3 : 2;
+  static constexpr int WARPS = ONE ? 8 : 4, CTAS = ONE ? FOURS / 2 : FOURS;
   static constexpr int HEADS = 4 * NC;                     // query heads of a tile
-  static constexpr int WARPS = 4;
   static constexpr int CB = kv_code_bytes<T>(D);           // bytes of a row's codes
   static constexpr int SB = T == kKvF16 ? 0 : D / 16;      // bytes of a row's scales
   static constexpr int SLOT = CH * (CB + SB);
-  static constexpr int SMEM = WARPS * SLOTS * SLOT;
+  static constexpr int PART = 4 * paged_part_floats(HEADS, D);  // bytes of a part
+  static constexpr int SMEM = WARPS * (ONE && PART > SLOTS * SLOT ? PART : SLOTS * SLOT);
 };
-constexpr int kMaxTile = 16;  // heads of a tile at most: a part is (m, l)[16], o[heads][D]
-__host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * kMaxTile; }
 
 // Position of 16-byte column `col` of a slot row, so that eight consecutive rows
 // of one column lie in different banks.
@@ -649,12 +668,22 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
   return upto;
 }
 
-template <int T, int D, int NC>
-__global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
+// ONE: a CTA to an item, whose eight warps share its chunks out and join through shared
+// memory, in one launch.  For at most as many items as SMs, and tables of at most
+// kOneCtaCtx positions a sequence, kOneCtaCtxMany where the items are half as many as the
+// SMs (Q8_0, 8 KV heads of 128, one launch against two; us on the device):
+//   1 sequence of 145 / 480 / 740 / 1000: 4.2 / 6.3 / 8.3 / 10.0 against 7.0 / 8.0 / 8.2 / 8.3
+//   16 of 480 / 740 / 1000 / 1500: 6.9 / 9.0 / 11.3 / 15.0 against 11.4 / 13.1 / 15.6 / 18.2
+//   64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
+// (not to 1500 for many: one long sequence among short ones would wait for its eight warps).
+constexpr int kOneCtaCtx = 768, kOneCtaCtxMany = 1024;
+
+template <int T, int D, int NC, bool ONE>
+__global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<T, D, NC, ONE>::CTAS)
     attn_paged_kernel(const ntx_paged_kv c, const float* __restrict__ q, int64_t qs, float* __restrict__ out,
                       int4* __restrict__ split, float* __restrict__ part, int Hq, const int* __restrict__ lens,
                       float scale, int* status) {
-  using F = PagedCfg<T, D, NC>;
+  using F = PagedCfg<T, D, NC, ONE>;
   constexpr int CH = F::CH, C = F::CB / 16, NB = D / 32, NS = CH / 16, NT = D / 16;
   extern __shared__ __align__(128) uint8_t ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -662,20 +691,31 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
   const int G = Hq / c.n_kv_heads, rtiles = (G + F::HEADS - 1) / F::HEADS;
   const int tiles = c.n_kv_heads * rtiles;
   const int wid = blockIdx.x * F::WARPS + warp, all_warps = gridDim.x * F::WARPS;
-  pdl_launch_dependents();  // the join's CTAs prepare themselves where there is room
-
-  // empty sequences: zeros
-  for (int s = wid; s < c.n_seqs; s += all_warps)
-    if (__ldg(lens + s) <= 0)
-      for (int64_t i = lane; i < (int64_t)Hq * D / 4; i += 32)
-        reinterpret_cast<float4*>(out + (int64_t)s * Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (!ONE) {
+    pdl_launch_dependents();  // the join's CTAs prepare themselves where there is room
+    // empty sequences: zeros
+    for (int s = wid; s < c.n_seqs; s += all_warps)
+      if (__ldg(lens + s) <= 0)
+        for (int64_t i = lane; i < (int64_t)Hq * D / 4; i += 32)
+          reinterpret_cast<float4*>(out + (int64_t)s * Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 
   __shared__ PagedParts s_parts[F::WARPS];
+  constexpr int kStart = ONE ? 0 : kItemUnits;
 
   // ---- this warp's part: its first chunk, and `todo` units from there
   PagedCursor cur;
   int64_t todo;
-  {
+  if constexpr (ONE) {
+    cur.s = blockIdx.x / tiles;
+    const int tile = blockIdx.x - cur.s * tiles;
+    cur.kvh = tile / rtiles;
+    cur.rt = tile - cur.kvh * rtiles;
+    cur.len = seq_len(c, lens, cur.s, status);
+    cur.n = (cur.len + CH - 1) / CH;
+    cur.ci = warp * cur.n / F::WARPS;
+    todo = (warp + 1) * cur.n / F::WARPS - cur.ci;
+  } else {
     const int k = (c.n_seqs + 31) >> 5;  // sequences to a lane
     int64_t mine;
     const int64_t upto = lane_units(c, lens, k, CH, tiles, mine, status);
@@ -707,6 +747,7 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     if (todo <= 0) return;
   }
   bool item_head = cur.ci == 0;  // false: the part begins inside an item
+  const bool empty = cur.len <= 0;
 
   // ---- loading: the ring's next slot takes K or V of chunk `ld`, 16 rows (one page) at a time
   const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D), scales_at = (int64_t)c.page_size * F::CB;
@@ -787,7 +828,7 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
         // the pages of the next chunk are used half a chunk from now
         if (--ld_left > 0) {
           const bool item = ld.ci + 1 == ld.n;
-          if (item) ld_left -= kItemUnits;
+          if (item) ld_left -= kStart;
           if (ld_left > 0) {
             ld.next(c, lens, rtiles, CH, status);
             look_up(item);
@@ -834,9 +875,30 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
   float o[NC][NT][2], m[NC], l[NC], to_log2[NC];
   float off[NC][NB];  // block types: minus the offset's share of a block's product
   bool fresh = true;
-  int rows = 0, head0 = 0;
+  int rows = min(F::HEADS, G - F::HEADS * cur.rt), head0 = cur.kvh * G + F::HEADS * cur.rt;
+  if constexpr (ONE) {  // a warp without a chunk
+#pragma unroll
+    for (int ct = 0; ct < NC; ++ct) {
+      m[ct] = -INFINITY;
+      l[ct] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[ct][n][0] = o[ct][n][1] = 0.f;
+    }
+  }
+  // this lane's elements of o, times f, to a row
+  auto store = [&](int ct, float* dst, float f) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (T == kKvF16) {
+        dst[16 * n + g] = o[ct][n][0] * f;
+        dst[16 * n + 8 + g] = o[ct][n][1] * f;
+      } else {
+        *reinterpret_cast<float2*>(dst + 16 * n + 2 * g) = make_float2(o[ct][n][0] * f, o[ct][n][1] * f);
+      }
+    }
+  };
 
-  for (;;) {
+  while (todo > 0) {
     if (fresh) {  // ---- an item's q, while its first keys are on the way
       rows = min(F::HEADS, G - F::HEADS * cur.rt);
       head0 = cur.kvh * G + F::HEADS * cur.rt;
@@ -1147,45 +1209,79 @@ __global__ void __launch_bounds__(128, PagedCfg<T, D, NC>::CTAS)
     // ---- end of an item, or of this warp's part
     --todo;
     const bool item_end = cur.ci + 1 == cur.n;
-    if (item_end) todo -= kItemUnits;
-    if (item_end || todo <= 0) {
-      const bool whole = item_end && item_head;
-      // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
-      const int64_t at = 2ll * wid + (item_head ? 1 : 0);
-      float* p = part + at * paged_part_floats(min(F::HEADS, G), D);
-      if (!whole && lane == 0) {  // the item's first warp and number of parts, where its output goes
-        const PagedParts parts = s_parts[warp];
-        // units up to the chunk after this one, less the item's own
-        const int64_t first = parts.begin(wid + 1) - max((int64_t)0, todo + (item_end ? kItemUnits : 0)) - cur.ci - 1;
-        const int w0 = parts.holder(first), n_parts = parts.holder(first + cur.n - 1) - w0 + 1;
-        split[at] = make_int4(w0, n_parts, cur.s, (head0 << 5) | rows);
-      }
+    if constexpr (!ONE) {
+      if (item_end) todo -= kItemUnits;
+      if (item_end || todo <= 0) {
+        const bool whole = item_end && item_head;
+        // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
+        const int64_t at = 2ll * wid + (item_head ? 1 : 0);
+        float* p = part + at * paged_part_floats(min(F::HEADS, G), D);
+        if (!whole && lane == 0) {  // the item's first warp and number of parts, where its output goes
+          const PagedParts parts = s_parts[warp];
+          // units up to the chunk after this one, less the item's own
+          const int64_t first = parts.begin(wid + 1) - max((int64_t)0, todo + (item_end ? kItemUnits : 0)) - cur.ci - 1;
+          const int w0 = parts.holder(first), n_parts = parts.holder(first + cur.n - 1) - w0 + 1;
+          split[at] = make_int4(w0, n_parts, cur.s, (head0 << 5) | rows);
+        }
 #pragma unroll
-      for (int ct = 0; ct < NC; ++ct) {
-        const int h = 4 * ct + t;
+        for (int ct = 0; ct < NC; ++ct) {
+          const int h = 4 * ct + t;
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
-        if (h >= rows) continue;
-        float* dst = whole ? out + ((int64_t)cur.s * Hq + head0 + h) * D : p + 2 * kMaxTile + h * D;
-        const float f = whole ? 1.f / l[ct] : 1.f;
-        if (!whole && g == 0) *reinterpret_cast<float2*>(p + 2 * h) = make_float2(m[ct], l[ct]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (T == kKvF16) {
-            dst[16 * n + g] = o[ct][n][0] * f;
-            dst[16 * n + 8 + g] = o[ct][n][1] * f;
+          for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
+          if (h >= rows) continue;
+          if (whole) {
+            store(ct, out + ((int64_t)cur.s * Hq + head0 + h) * D, 1.f / l[ct]);
           } else {
-            *reinterpret_cast<float2*>(dst + 16 * n + 2 * g) = make_float2(o[ct][n][0] * f, o[ct][n][1] * f);
+            if (g == 0) *reinterpret_cast<float2*>(p + 2 * h) = make_float2(m[ct], l[ct]);
+            store(ct, p + 2 * kMaxTile + h * D, 1.f);
           }
         }
+        if (todo <= 0) break;
+        item_head = true;
+        fresh = true;
       }
-      if (todo <= 0) break;
-      item_head = true;
-      fresh = true;
     }
     cur.next(c, lens, rtiles, CH, status);
   }
   cp_async_wait<0>();
+
+  if constexpr (ONE) {
+    auto at = [&](int w) { return reinterpret_cast<float*>(ring + w * F::PART); };
+    __syncthreads();  // every warp is done with its ring
+#pragma unroll
+    for (int ct = 0; ct < NC; ++ct) {
+      const int h = 4 * ct + t;
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
+      if (h >= rows) continue;
+      if (g == 0) *reinterpret_cast<float2*>(at(warp) + 2 * h) = make_float2(m[ct], l[ct]);
+      store(ct, at(warp) + 2 * kMaxTile + h * D, 1.f);
+    }
+    __syncthreads();
+    const int s = blockIdx.x / tiles;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += F::WARPS * 32) {
+      const int h = i / (D / 4);
+      float2 ml[F::WARPS];
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < F::WARPS; ++w) {
+        ml[w] = *reinterpret_cast<const float2*>(at(w) + 2 * h);
+        M = fmaxf(M, ml[w].x);
+      }
+      if (M == -INFINITY) M = 0.f;
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < F::WARPS; ++w) {
+        const float f = ex2(ml[w].x - M);
+        const float4 x = reinterpret_cast<const float4*>(at(w) + 2 * kMaxTile)[i];
+        L = fmaf(ml[w].y, f, L);
+        O.x = fmaf(x.x, f, O.x); O.y = fmaf(x.y, f, O.y); O.z = fmaf(x.z, f, O.z); O.w = fmaf(x.w, f, O.w);
+      }
+      const float f = empty ? 0.f : 1.f / L;
+      reinterpret_cast<float4*>(out + ((int64_t)s * Hq + head0) * D)[i] = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+    }
+  }
 }
 
 // Joins the parts of the items that several warps hold: with M the largest m,

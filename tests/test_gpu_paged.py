@@ -171,9 +171,9 @@ def attend(cache, q, lens, hq, scale, ws=None, stream=None, q_stride=None, out=N
     return out
 
 
-def check_attention(kind, hq, hkv, d, ps, lens, seed, q_sigma=1.0, scale=None):
+def check_attention(kind, hq, hkv, d, ps, lens, seed, q_sigma=1.0, scale=None, max_pages=None):
     torch = _t()
-    c = Cache(kind, hkv, d, ps, lens, seed).fill(seed + 1)
+    c = Cache(kind, hkv, d, ps, lens, seed, max_pages=max_pages).fill(seed + 1)
     q = (np.random.RandomState(seed + 2).standard_normal((len(lens), hq, d)) * q_sigma).astype(np.float32)
     scale = np.float32(d ** -0.5 if scale is None else scale).item()
     got = attend(c, torch.from_numpy(q).cuda(), lens, hq, scale).cpu().numpy().astype(np.float64)
@@ -346,8 +346,10 @@ def test_places_outside_the_cache_are_skipped_and_reported(kind):
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 1), (15, 3), (24, 2)])
-def test_attention_types_and_heads(kind, d, hq, hkv):
-    check_attention(kind, hq, hkv, d, 32, [1, 77, 200], 100 + d + hq)
+@pytest.mark.parametrize("max_pages", [None, 40])
+def test_attention_types_and_heads(kind, d, hq, hkv, max_pages):
+    """In a table for 224 positions a sequence (one CTA to an item) and in one for 1280 (parts and their join)."""
+    check_attention(kind, hq, hkv, d, 32, [1, 77, 200], 100 + d + hq, max_pages=max_pages)
 
 
 @pytest.mark.parametrize("kind", TYPES)
@@ -371,6 +373,25 @@ def test_attention_many_sequences(kind):
     rs = np.random.RandomState(9)
     lens = [int(x) for x in rs.randint(0, 90, 300)]
     check_attention(kind, 8, 2, 64, 16, lens, 400)
+    check_attention(kind, 8, 2, 64, 16, lens, 403, max_pages=50)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("d,hq,hkv", [(64, 12, 2), (128, 8, 2), (128, 40, 1), (256, 24, 3)])
+def test_attention_up_to_both_sides_of_one_cta(kind, d, hq, hkv):
+    """Every number of chunks a CTA's warps can have, to the longest table that one CTA to an item takes; then one
+    page more."""
+    lens = [0, 1, 16, 17, 31, 32, 33, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 300, 400, 511, 512, 767, 768]
+    check_attention(kind, hq, hkv, d, 16, lens, 410 + d, max_pages=48)
+    check_attention(kind, hq, hkv, d, 16, lens, 410 + d, max_pages=49)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_attention_one_cta_for_many_items(kind):
+    """80 items (more than half of the SMs), tables of 1024 positions and of a page more."""
+    lens = [1024, 1000, 0, 1, 33, 700, 513, 1023] + [5] * 32
+    check_attention(kind, 6, 2, 64, 32, lens, 420, max_pages=32)
+    check_attention(kind, 6, 2, 64, 32, lens, 420, max_pages=33)
 
 
 def test_attention_most_sequences():
