@@ -166,13 +166,26 @@ cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs
   using O = PagedCfg<T, D, NC, true>;
   const int64_t items = (int64_t)kv.n_seqs * kv.n_kv_heads * ((G + O::HEADS - 1) / O::HEADS);
   const int64_t ctx = (int64_t)kv.max_pages * kv.page_size;
-  if (items <= sm_count() && ctx <= (2 * items < sm_count() ? kOneCtaCtx : kOneCtaCtxMany)) {
+  int ctas = 1;  // of a cluster
+  while (ctas < 8 && ctx > ctas * O::WARPS * O::CH && items * ctas * 2 <= sm_count() * 3 / 4) ctas *= 2;
+  const bool many = ctas == 1 && 2 * items >= sm_count();
+  if (items <= sm_count() && ctx <= (many ? kOneCtaCtxMany : kOneCtaCtx * ctas)) {
     static std::atomic<unsigned long long> done_one{0};
     const cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done_one);
     if (e != cudaSuccess) return e;
-    attn_paged_kernel<T, D, NC, true><<<(int)items, O::WARPS * 32, O::SMEM, stream>>>(
-        kv, q, qs, out, nullptr, nullptr, Hq, lens, scale, device_status_ptr());
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * ctas));
+    cfg.blockDim = dim3(O::WARPS * 32);
+    cfg.dynamicSmemBytes = O::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_paged_kernel<T, D, NC, true>, kv, q, qs, out, (int4*)nullptr, (float*)nullptr,
+                              Hq, lens, scale, device_status_ptr());
   }
   int4* split = static_cast<int4*>(ws);
   float* part = reinterpret_cast<float*>(split + 2 * (size_t)warps);

@@ -2,6 +2,8 @@
 // the cache's write and read-back, and decode attention over it.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -583,7 +585,8 @@ struct PagedCfg {
   static constexpr int SB = T == kKvF16 ? 0 : D / 16;      // bytes of a row's scales
   static constexpr int SLOT = CH * (CB + SB);
   static constexpr int PART = 4 * paged_part_floats(HEADS, D);  // bytes of a part
-  static constexpr int SMEM = WARPS * (ONE && PART > SLOTS * SLOT ? PART : SLOTS * SLOT);
+  static constexpr int RING = WARPS * SLOTS * SLOT, PARTS = (WARPS + 1) * PART;  // the warps' and the CTA's
+  static constexpr int SMEM = ONE && PARTS > RING ? PARTS : RING;
 };
 
 // Position of 16-byte column `col` of a slot row, so that eight consecutive rows
@@ -668,14 +671,20 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
   return upto;
 }
 
-// ONE: a CTA to an item, whose eight warps share its chunks out and join through shared
-// memory, in one launch.  For at most as many items as SMs, and tables of at most
-// kOneCtaCtx positions a sequence, kOneCtaCtxMany where the items are half as many as the
-// SMs (Q8_0, 8 KV heads of 128, one launch against two; us on the device):
-//   1 sequence of 145 / 480 / 740 / 1000: 4.2 / 6.3 / 8.3 / 10.0 against 7.0 / 8.0 / 8.2 / 8.3
-//   16 of 480 / 740 / 1000 / 1500: 6.9 / 9.0 / 11.3 / 15.0 against 11.4 / 13.1 / 15.6 / 18.2
+// ONE: a cluster of 1 to 8 CTAs to an item, whose warps share its chunks out and join
+// through shared memory, the CTAs through the cluster's, in one launch.  Taken for at
+// most as many items as SMs, with as many CTAs as give each warp one chunk of the longest
+// sequence that the table can hold while they are at most three quarters of the SMs (all
+// clusters of 8 are then resident at once), and tables of at most kOneCtaCtx positions
+// for each of the CTAs; kOneCtaCtxMany where one CTA is all there is and the items are
+// half as many as the SMs.  Against parts and their join, Q8_0, 8 KV heads of 128, us on
+// the device:
+//   1 sequence of 145 / 480 / 1000 / 2049 / 4000 / 6000:
+//     4.2 / 6.2 / 6.9 / 7.9 / 8.4 / 10.2 against 7.0 / 8.0 / 8.3 / 8.8 / 9.7 / 10.4
+//   3 of 480 / 1000 / 2049: 6.3 / 7.0 / 10.1 against 8.4 / 8.9 / 10.6
+//   16 of 480 / 1000: 7.1 / 11.3 against 11.4 / 15.6
 //   64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
-// (not to 1500 for many: one long sequence among short ones would wait for its eight warps).
+// (not further for many: one long sequence among short ones would wait for its own warps).
 constexpr int kOneCtaCtx = 768, kOneCtaCtxMany = 1024;
 
 template <int T, int D, int NC, bool ONE>
@@ -706,15 +715,19 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
   // ---- this warp's part: its first chunk, and `todo` units from there
   PagedCursor cur;
   int64_t todo;
+  const int ctas = ONE ? (int)cooperative_groups::this_cluster().num_blocks() : 1;  // of an item
+  const int rank = ONE ? (int)cooperative_groups::this_cluster().block_rank() : 0;
   if constexpr (ONE) {
-    cur.s = blockIdx.x / tiles;
-    const int tile = blockIdx.x - cur.s * tiles;
+    const int item = blockIdx.x / ctas;
+    cur.s = item / tiles;
+    const int tile = item - cur.s * tiles;
     cur.kvh = tile / rtiles;
     cur.rt = tile - cur.kvh * rtiles;
     cur.len = seq_len(c, lens, cur.s, status);
     cur.n = (cur.len + CH - 1) / CH;
-    cur.ci = warp * cur.n / F::WARPS;
-    todo = (warp + 1) * cur.n / F::WARPS - cur.ci;
+    const int w = rank * F::WARPS + warp, warps = ctas * F::WARPS;
+    cur.ci = w * cur.n / warps;
+    todo = (w + 1) * cur.n / warps - cur.ci;
   } else {
     const int k = (c.n_seqs + 31) >> 5;  // sequences to a lane
     int64_t mine;
@@ -748,6 +761,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
   }
   bool item_head = cur.ci == 0;  // false: the part begins inside an item
   const bool empty = cur.len <= 0;
+  const int item_s = cur.s;
 
   // ---- loading: the ring's next slot takes K or V of chunk `ld`, 16 rows (one page) at a time
   const int64_t head_bytes = (int64_t)c.page_size * kv_row_bytes<T>(D), scales_at = (int64_t)c.page_size * F::CB;
@@ -1258,28 +1272,55 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
       store(ct, at(warp) + 2 * kMaxTile + h * D, 1.f);
     }
     __syncthreads();
-    const int s = blockIdx.x / tiles;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += F::WARPS * 32) {
+    // parts `at(0)` to `at(n - 1)` joined: elements 4 i to 4 i + 3 of the item's rows, and the row's (m, l)
+    auto join = [&](auto part_at, int n, int i, float2& ml) {
       const int h = i / (D / 4);
-      float2 ml[F::WARPS];
       float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < F::WARPS; ++w) {
-        ml[w] = *reinterpret_cast<const float2*>(at(w) + 2 * h);
-        M = fmaxf(M, ml[w].x);
-      }
-      if (M == -INFINITY) M = 0.f;
+#pragma unroll 8
+      for (int w = 0; w < n; ++w) M = fmaxf(M, part_at(w)[2 * h]);
+      const float base = M == -INFINITY ? 0.f : M;
       float L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < F::WARPS; ++w) {
-        const float f = ex2(ml[w].x - M);
-        const float4 x = reinterpret_cast<const float4*>(at(w) + 2 * kMaxTile)[i];
-        L = fmaf(ml[w].y, f, L);
-        O.x = fmaf(x.x, f, O.x); O.y = fmaf(x.y, f, O.y); O.z = fmaf(x.z, f, O.z); O.w = fmaf(x.w, f, O.w);
+#pragma unroll 8
+      for (int w = 0; w < n; ++w) {
+        const float* p = part_at(w);
+        const float2 x = *reinterpret_cast<const float2*>(p + 2 * h);
+        const float4 y = reinterpret_cast<const float4*>(p + 2 * kMaxTile)[i];
+        const float f = ex2(x.x - base);
+        L = fmaf(x.y, f, L);
+        O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y); O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
       }
-      const float f = empty ? 0.f : 1.f / L;
-      reinterpret_cast<float4*>(out + ((int64_t)s * Hq + head0) * D)[i] = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+      ml = make_float2(M, L);
+      return O;
+    };
+    auto finish = [&](int i, float4 O, float L) {
+      const float f = empty ? 0.f : 1.f / L;  // an empty sequence: zeros
+      reinterpret_cast<float4*>(out + ((int64_t)item_s * Hq + head0) * D)[i] =
+          make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+    };
+    const int pieces = rows * (D / 4);
+    float2 ml;
+    if (ctas == 1) {
+      for (int i = threadIdx.x; i < pieces; i += F::WARPS * 32) {
+        const float4 O = join(at, F::WARPS, i, ml);
+        finish(i, O, ml.y);
+      }
+    } else {
+      // the CTA's part, then every CTA joins its share of the cluster's
+      namespace cg = cooperative_groups;
+      cg::cluster_group cluster = cg::this_cluster();
+      float* own = at(F::WARPS);
+      for (int i = threadIdx.x; i < pieces; i += F::WARPS * 32) {
+        const float4 O = join(at, F::WARPS, i, ml);
+        reinterpret_cast<float4*>(own + 2 * kMaxTile)[i] = O;
+        if (i % (D / 4) == 0) *reinterpret_cast<float2*>(own + 2 * (i / (D / 4))) = ml;
+      }
+      cluster.sync();
+      for (int i = rank * F::WARPS * 32 + threadIdx.x; i < pieces; i += ctas * F::WARPS * 32) {
+        const float4 O = join([&](int r) { return (const float*)cluster.map_shared_rank(own, r); }, ctas, i, ml);
+        finish(i, O, ml.y);
+      }
+      cluster.sync();  // nobody's shared memory goes before it has been read
     }
   }
 }

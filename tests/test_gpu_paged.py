@@ -387,6 +387,15 @@ def test_attention_up_to_both_sides_of_one_cta(kind, d, hq, hkv):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("d,hq,hkv", [(64, 16, 1), (128, 4, 1), (256, 8, 1)])
+@pytest.mark.parametrize("top", [128, 256, 272, 512, 528, 1024, 1040, 2048, 2064, 6144, 6160])
+def test_attention_clusters(kind, d, hq, hkv, top):
+    """Few items: one CTA to eight for each, by the positions a table can hold, and parts beyond; a full sequence, an
+    empty one, and one that leaves most warps without a chunk."""
+    check_attention(kind, hq, hkv, d, 16, [top, 0, 35], 430 + top, max_pages=top // 16)
+
+
+@pytest.mark.parametrize("kind", TYPES)
 def test_attention_one_cta_for_many_items(kind):
     """80 items (more than half of the SMs), tables of 1024 positions and of a page more."""
     lens = [1024, 1000, 0, 1, 33, 700, 513, 1023] + [5] * 32
