@@ -286,7 +286,7 @@ NTX_API uint64_t ntx_paged_kv_bytes(int type, int n_kv_heads, int head_dim, int 
  *   theta^(-2i/rot_dim), i < rot_dim/2, with (a, b) = elements (2i, 2i+1)
  *   (NTX_ROPE_ADJACENT, the pairing of ntx_rope) or (i, i + rot_dim/2)
  *   (NTX_ROPE_HALVES); elements from rot_dim on are only normed.
- * Angles are formed in fp64, the rest in fp32.
+ * Angles are formed in fp64 (off by up to 2^-51 of the angle), the rest in fp32.
  *   q, q_out: device fp32, token n's n_q_heads x head_dim values start at
  *   n * q_stride floats; k, k_out: n_kv_heads x head_dim at n * k_stride.
  *   q_out may be q and k_out may be k; any other overlap of an output with an
@@ -345,7 +345,8 @@ NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_st
  *   aligned; scratch only, contents on entry ignored.  Calls that may overlap
  *   on the GPU need workspaces of their own.
  * Limits: n_kv_heads | n_q_heads, at most 64 query heads per KV head; scale
- * finite; q and out 16-byte aligned, q_stride a multiple of 4.
+ * finite; q and out 16-byte aligned, q_stride a multiple of 4; |scale q| below
+ * 2^116 over block types.
  * A length below 0 counts as 0 and one past max_pages * page_size as that; a
  * page outside the pool reads as keys and values of zero (status 5 for each).
  * Cache rows past a sequence's length are not used, whatever they hold. */

@@ -270,12 +270,14 @@ __device__ __forceinline__ float rope_rsqrt(float x) {
 
 // Cosine and sine of t half turns: t less the nearest multiple of a quarter turn is
 // exact in fp64 and rounds to fp32 within 2^-27 of a half turn, 2e-8; sine and cosine
-// of at most an eighth of a turn are fp32's.
+// of at most an eighth of a turn are fp32's.  The multiple is rounded by adding
+// 1.5 2^52, whose low word then counts quarter turns: any t below 2^50, where an fp64
+// angle still tells quarters apart (a theta below 1 brings angles past 2^31).
 __device__ __forceinline__ float2 rope_turn(double t) {
-  const double n = rint(2.0 * t);
+  const double m = fma(2.0, t, 6755399441055744.0), n = m - 6755399441055744.0;
   float s, c;
   sincospif((float)fma(-0.5, n, t), &s, &c);
-  const int k = (int)n;  // |t| < 2^31 / pi
+  const unsigned k = (unsigned)__double2loint(m);
   const float x = (k & 1) ? s : c, y = (k & 1) ? c : s;
   return make_float2(((k + 1) & 2) ? -x : x, (k & 2) ? -y : y);
 }

@@ -658,6 +658,28 @@ def test_norm_rope_matches(n, hq, hk, d, rot, halves):
         assert np.array_equal(dev[i].cpu().numpy(), x[i])  # the input stays
 
 
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norm_rope_angles_past_32_bits(d, halves):
+    """theta below 1: frequencies above 1, quarter turns past 2^31.  theta = 2^-8 and rot_dim 16 make the frequency of
+    pair i 2^i, so that the reference's angles are exact.  The kernel's: three roundings of 2^-53 (the frequency, by
+    1 / pi, by the position) and what exp2 is off by (2 at most), 2^-51 of the angle at most; at 2^38 that is 2^-13."""
+    torch = _t()
+    pos = np.array([2 ** 31 - 1, 2 ** 31 - 12345, 2 ** 30 + 7, 123456789, 1], np.int32)
+    n, hq, hk, rot, theta = len(pos), 3, 2, 16, 2.0 ** -8
+    x = np.random.RandomState(d).standard_normal((n, hq + hk, d)).astype(np.float32)
+    b = torch.from_numpy(x).cuda()
+    w = (hq + hk) * d
+    ntx.ntx_qk_norm_rope(b, b.view(-1)[hq * d:], b, b.view(-1)[hq * d:], w, w, None, None, torch.from_numpy(pos).cuda(), n,
+                         hq, hk, d, rot, int(halves), theta, 1e-6)
+    ref, size = norm_rope_ref(x, None, pos, rot, halves, theta, np.float64(np.float32(1e-6)))
+    i = np.arange(rot // 2)
+    turn = np.zeros((n, 1, d))
+    turn[:, 0, i if halves else 2 * i] = turn[:, 0, i + rot // 2 if halves else 2 * i + 1] = \
+        pos.astype(np.float64)[:, None] * np.exp2(i)
+    assert np.all(np.abs(b.cpu().numpy() - ref) <= (2e-6 + turn * 2.0 ** -51) * size)
+
+
 def test_norm_rope_in_place_in_a_fused_row():
     """q and k inside the rows of one projection, in place, at an odd stride; v and the gaps stay."""
     torch = _t()
