@@ -146,13 +146,12 @@ def lib():
 
 
 def _p(x):
-    if x is None:
-        return None
-    get = getattr(x, "data_ptr", None)  # a tensor, the argument of nearly every call
-    if get is not None:
-        return get()
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
+    try:
+        return x.data_ptr()  # a tensor, the argument of nearly every call
+    except AttributeError:
+        pass
     if isinstance(x, ctypes.c_void_p):
         return x.value
     raise TypeError(f"cannot take a pointer from {type(x).__name__}")

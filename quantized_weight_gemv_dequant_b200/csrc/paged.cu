@@ -157,39 +157,87 @@ size_t paged_ws(const ntx_paged_kv* kv, int n_q_heads) {
   return n;
 }
 
+template <class O>
+void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int64_t grid, int ctas, cudaStream_t stream) {
+  cfg->gridDim = dim3((unsigned)grid);
+  cfg->blockDim = dim3(O::WARPS * 32);
+  cfg->dynamicSmemBytes = O::SMEM;
+  cfg->stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)ctas;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// How a cluster of CTAs to an item runs: as many CTAs as give each warp one chunk of the
+// longest sequence that the table can hold, or the most of which all clusters are resident
+// at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each).
+struct OneGrid {
+  int64_t items, work;  // work: (position, head) pairs of a warp at most; 0: more items than fit
+  int most, ctas;
+};
+template <int T, int D, int NC>
+cudaError_t one_grid(const ntx_paged_kv& kv, int G, OneGrid* grid) {
+  using O = PagedCfg<T, D, NC, true>;
+  static std::atomic<unsigned long long> done{0};
+  static std::atomic<int> fit[9];  // 1 more than the clusters of that many CTAs that are resident at once
+  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done);
+  if (e != cudaSuccess) return e;
+  OneGrid g{(int64_t)kv.n_seqs * kv.n_kv_heads * ((G + O::HEADS - 1) / O::HEADS), 0, 0, 0};
+  const int64_t chunks = ((int64_t)kv.max_pages * kv.page_size + O::CH - 1) / O::CH;
+  for (int c = 1; c <= 8; ++c) {
+    int n = fit[c].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      one_config<O>(&cfg, attr, c, c, nullptr);
+      if ((e = cudaOccupancyMaxActiveClusters(&n, attn_paged_kernel<T, D, NC, true>, &cfg)) != cudaSuccess) return e;
+      fit[c].store(++n, std::memory_order_relaxed);
+    }
+    if (g.items >= n) continue;
+    g.most = c;
+    if (g.ctas * O::WARPS < chunks) g.ctas = c;
+  }
+  if (g.ctas) g.work = (chunks + g.ctas * O::WARPS - 1) / (g.ctas * O::WARPS) * O::CH * O::HEADS;
+  *grid = g;
+  return cudaSuccess;
+}
+
+template <int T, int D, int NC>
+cudaError_t launch_attn_one(const OneGrid& g, const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
+                            const int32_t* lens, float scale, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  one_config<PagedCfg<T, D, NC, true>>(&cfg, attr, g.items * g.ctas, g.ctas, stream);
+  return cudaLaunchKernelEx(&cfg, attn_paged_kernel<T, D, NC, true>, kv, q, qs, out, (int4*)nullptr, (float*)nullptr, Hq,
+                            lens, scale, device_status_ptr());
+}
+
 template <int T, int D, int NC>
 cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs, float* out, int Hq,
                               const int32_t* lens, float scale, void* ws, cudaStream_t stream) {
   using F = PagedCfg<T, D, NC, false>;
   static std::atomic<unsigned long long> done{0};
   const int grid = sm_count() * F::CTAS, warps = grid * F::WARPS, G = Hq / kv.n_kv_heads;
-  using O = PagedCfg<T, D, NC, true>;
-  const int64_t items = (int64_t)kv.n_seqs * kv.n_kv_heads * ((G + O::HEADS - 1) / O::HEADS);
   const int64_t ctx = (int64_t)kv.max_pages * kv.page_size;
-  int ctas = 1;  // of a cluster
-  while (ctas < 8 && ctx > ctas * O::WARPS * O::CH && items * ctas * 2 <= sm_count() * 3 / 4) ctas *= 2;
-  const bool many = ctas == 1 && 2 * items >= sm_count();
-  if (items <= sm_count() && ctx <= (many ? kOneCtaCtxMany : kOneCtaCtx * ctas)) {
-    static std::atomic<unsigned long long> done_one{0};
-    const cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done_one);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * ctas));
-    cfg.blockDim = dim3(O::WARPS * 32);
-    cfg.dynamicSmemBytes = O::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_paged_kernel<T, D, NC, true>, kv, q, qs, out, (int4*)nullptr, (float*)nullptr,
-                              Hq, lens, scale, device_status_ptr());
+  cudaError_t e;
+  if (ctx <= 8 * kOneCtaCtx) {
+    OneGrid one, narrow;
+    if ((e = one_grid<T, D, NC>(kv, G, &one)) != cudaSuccess) return e;
+    const bool many = one.most == 1 && 2 * one.items >= sm_count();
+    if (one.work && ctx <= (many ? kOneCtaCtxMany : kOneCtaCtx * one.most)) {
+      if constexpr (NC > 1) {  // four heads to a tile where a warp's work is no more for it
+        if ((e = one_grid<T, D, 1>(kv, G, &narrow)) != cudaSuccess) return e;
+        if (narrow.work && narrow.work <= one.work)
+          return launch_attn_one<T, D, 1>(narrow, kv, q, qs, out, Hq, lens, scale, stream);
+      }
+      return launch_attn_one<T, D, NC>(one, kv, q, qs, out, Hq, lens, scale, stream);
+    }
   }
   int4* split = static_cast<int4*>(ws);
   float* part = reinterpret_cast<float*>(split + 2 * (size_t)warps);
-  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, false>, F::SMEM, done);
+  e = allow_smem(attn_paged_kernel<T, D, NC, false>, F::SMEM, done);
   if (e != cudaSuccess) return e;
   attn_paged_kernel<T, D, NC, false><<<grid, F::WARPS * 32, F::SMEM, stream>>>(kv, q, qs, out, split, part, Hq, lens, scale,
                                                                        device_status_ptr());

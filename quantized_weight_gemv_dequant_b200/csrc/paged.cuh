@@ -47,10 +47,11 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 // A warp of the write and of the read handles one row's piece of kPiece elements,
 // four consecutive ones to a lane at a time (eight lanes a block of 32), all its
 // loads in flight at once; a row's place is looked up once a piece.  On B200, 24001
-// tokens of 8 heads of 128 from Q8_0: 44 us, 5.6 TB/s, 0.86 of a copy's bandwidth;
-// 16384 tokens to Q4_0 and back: 42 and 28 us, 3.6 and 5.4 TB/s.  The write to 4 bits
-// is bound by its 135 instructions for each 128 elements (ALU pipe at 0.66, issue at
-// 0.75), everything else by memory.  Pieces of 1024 elements are 3 % faster on long
+// tokens of 8 heads of 128 from Q8_0: 43 us, 5.7 TB/s, 0.87 of a copy's bandwidth;
+// 16384 tokens to Q4_0 and back: 65 us (with a search of the first largest by ballot
+// and separate checks of zeros and infinities in every block: 69), 28 of them the read
+// at 5.4 TB/s.  The write to 4 bits is bound by its instructions, everything else by
+// memory.  Pieces of 1024 elements are 3 % faster on long
 // prompts and 25 % slower on one token.
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
 constexpr int kTokenWarps = 4;  // tokens of a CTA
@@ -82,7 +83,8 @@ struct PieceAt {
 // within 2^-14 of the quotient (which is at most 127, or 8), tells it unless it is
 // next to a half; rounding is by adding 1.5 2^23 (and 8 for Q4_0), whose lowest
 // byte is then the code.  Next to a half, and where rcp(d) overflows, the quotient
-// itself decides.
+// itself decides.  Blocks of zeros or with an infinity or a NaN show there too: one
+// of their products is not a number, and a warp without any has nothing to look at.
 template <int T>
 __device__ __forceinline__ uint32_t quotient_code(float w, float d) {
   const float x = fabsf(w / d), f = floorf(x);
@@ -90,33 +92,30 @@ __device__ __forceinline__ uint32_t quotient_code(float w, float d) {
   q = (w < 0.f) != (d < 0.f) ? -q : q;
   return (uint32_t)(T == kKvQ8 ? min(127, max(-127, q)) : min(15, max(0, q + 8))) & 255u;
 }
-template <int T>
-__device__ __forceinline__ uint32_t quotient_codes(const float w[4], float d) {
-  constexpr float kMagic = T == kKvQ8 ? 12582912.f : 12582920.f;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  uint32_t m[4];
-  bool sure = true;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = w[i] * r, y = x + kMagic;
-    sure &= fabsf(x - (y - kMagic)) < 0.5f - 0x1p-14f;
-    m[i] = __float_as_uint(y);
-  }
-  if (sure) {
-    const uint32_t c = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
-    return T == kKvQ4 ? c - (c >> 4 & 0x01010101u) : c;  // 16, the largest's opposite, is 15
-  }
-  uint32_t codes = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) codes |= quotient_code<T>(w[i], d) << (8 * i);
-  return codes;
-}
 __device__ __forceinline__ float max_nan(float x, float y, float z) {  // NaN if any is
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
+
+// Codes by the reciprocal; false where one of the four is next to a half or is not a number.
+template <int T>
+__device__ __forceinline__ bool reciprocal_codes(const float w[4], float d, uint32_t* codes) {
+  constexpr float kMagic = T == kKvQ8 ? 12582912.f : 12582920.f;
+  float r, e[4];
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y = fmaf(w[i], r, kMagic);
+    e[i] = fabsf(fmaf(w[i], r, kMagic - y));
+    m[i] = __float_as_uint(y);
+  }
+  const uint32_t c = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+  *codes = T == kKvQ4 ? c - (c >> 4 & 0x01010101u) : c;  // 16, the largest's opposite, is 15
+  return max_nan(max_nan(e[0], e[1], e[2]), e[3], 0.f) < 0.5f - 0x1p-14f;
+}
+__device__ __forceinline__ float larger(float x, float y) { return fabsf(y) > fabsf(x) ? y : x; }
 
 template <int T, int D>
 __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_paged_kv c, const float* __restrict__ k,
@@ -163,36 +162,48 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
         *reinterpret_cast<uint2*>(at.code(i)) = h;
       }
     } else {
-      float top = max_nan(max_nan(fabsf(w[i][0]), fabsf(w[i][1]), fabsf(w[i][2])), fabsf(w[i][3]), 0.f);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o), 0.f);
-      const bool finite = top < INFINITY;
       float d;
       if constexpr (T == kKvQ8) {
+        float top = fmaxf(fmaxf(fabsf(w[i][0]), fabsf(w[i][1])), fmaxf(fabsf(w[i][2]), fabsf(w[i][3])));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         d = top / 127.0f;
       } else {
-        // the first element of the largest magnitude decides the sign
-        float m = 0.f;
-        bool has = false;
+        // the first element of the largest magnitude: a tie stays with the lower lane, which has the earlier one
+        float m = larger(larger(w[i][0], w[i][1]), larger(w[i][2], w[i][3]));
 #pragma unroll
-        for (int j = 3; j >= 0; --j)
-          if (fabsf(w[i][j]) == top) {
-            m = w[i][j];
-            has = true;
-          }
-        const unsigned lanes = __ballot_sync(0xffffffffu, has) >> (lane & 24) & 255u;
-        m = __shfl_sync(0xffffffffu, m, (lane & 24) + (lanes ? __ffs(lanes) - 1 : 0));
-        d = (top > 0.f ? m : 0.f) * -0.125f;
+        for (int o = 1; o < 8; o <<= 1) m = larger(m, __shfl_down_sync(0xffffffffu, m, o, 8));
+        d = __shfl_sync(0xffffffffu, m, 0, 8) * -0.125f;
       }
-      // zeros and blocks that are not finite: codes of zero
-      const uint32_t codes = top > 0.f && finite ? quotient_codes<T>(w[i], d) : T == kKvQ8 ? 0u : 0x08080808u;
+      uint32_t codes;
+      const bool sure = reciprocal_codes<T>(w[i], d, &codes);
+      uint16_t scale = float_to_half_bits(d);
+      if (__any_sync(0xffffffffu, on && !sure)) {  // zeros and what is not finite too: 0 or an infinity times r
+        bool bad = false, some = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bad |= !(fabsf(w[i][j]) < INFINITY);
+          some |= w[i][j] != 0.f;
+        }
+        const unsigned block = 255u << (lane & 24);
+        bad = __ballot_sync(0xffffffffu, bad) & block;
+        some = __ballot_sync(0xffffffffu, some) & block;
+        if (bad || !some) {  // codes of zero
+          codes = T == kKvQ8 ? 0u : 0x08080808u;
+          scale = bad ? 0x7FFF : T == kKvQ8 ? 0 : 0x8000;
+        } else if (!sure) {
+          codes = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) codes |= quotient_code<T>(w[i][j], d) << (8 * j);
+        }
+      }
       if constexpr (T == kKvQ8) {
         if (on) *reinterpret_cast<uint32_t*>(at.code(i)) = codes;
       } else {
         const uint32_t hi = __shfl_down_sync(0xffffffffu, codes, 4, 8);  // elements 16 further on
         if (on && sub < 4) *reinterpret_cast<uint32_t*>(at.code(i)) = codes | (hi << 4);
       }
-      if (on && sub == 0) *at.scale(i) = finite ? float_to_half_bits(d) : (uint16_t)0x7FFF;
+      if (on && sub == 0) *at.scale(i) = scale;
     }
   }
 }
