@@ -174,8 +174,8 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int64_t grid
 // longest sequence that the table can hold, or the most of which all clusters are resident
 // at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each).
 struct OneGrid {
-  int64_t items, work;  // work: (position, head) pairs of a warp at most; 0: more items than fit
-  int most, ctas;
+  int64_t items, work;  // work: a warp's positions times heads at most
+  int most, ctas;       // 0: more items than CTAs are resident
 };
 template <int T, int D, int NC>
 cudaError_t one_grid(const ntx_paged_kv& kv, int G, OneGrid* grid) {
@@ -223,13 +223,13 @@ cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs
   const int64_t ctx = (int64_t)kv.max_pages * kv.page_size;
   cudaError_t e;
   if (ctx <= 8 * kOneCtaCtx) {
-    OneGrid one, narrow;
+    OneGrid one;
     if ((e = one_grid<T, D, NC>(kv, G, &one)) != cudaSuccess) return e;
-    const bool many = one.most == 1 && 2 * one.items >= sm_count();
-    if (one.work && ctx <= (many ? kOneCtaCtxMany : kOneCtaCtx * one.most)) {
+    if (ctx <= kOneCtaCtx * one.most) {
       if constexpr (NC > 1) {  // four heads to a tile where a warp's work is no more for it
+        OneGrid narrow;
         if ((e = one_grid<T, D, 1>(kv, G, &narrow)) != cudaSuccess) return e;
-        if (narrow.work && narrow.work <= one.work)
+        if (narrow.most && narrow.work <= one.work)
           return launch_attn_one<T, D, 1>(narrow, kv, q, qs, out, Hq, lens, scale, stream);
       }
       return launch_attn_one<T, D, NC>(one, kv, q, qs, out, Hq, lens, scale, stream);

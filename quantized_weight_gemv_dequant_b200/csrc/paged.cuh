@@ -51,8 +51,8 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 // 16384 tokens to Q4_0 and back: 65 us (with a search of the first largest by ballot
 // and separate checks of zeros and infinities in every block: 69), 28 of them the read
 // at 5.4 TB/s.  The write to 4 bits is bound by its instructions, everything else by
-// memory.  Pieces of 1024 elements are 3 % faster on long
-// prompts and 25 % slower on one token.
+// memory.  Pieces of 1024 elements are 3 % faster on long prompts and 25 % slower on one
+// token.
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
 constexpr int kTokenWarps = 4;  // tokens of a CTA
 
@@ -583,13 +583,14 @@ __host__ __device__ constexpr int paged_part_floats(int rows, int D) { return ro
 
 // Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.  A chunk is
 // 2 to 8 KiB of keys: 64 positions of the narrow rows (4-bit rows of 128: 131071
-// positions in 49 us, 52 with 32), 16 of fp16 rows of 256.  The CTAs are those whose
+// positions in 49 us, 52 with 32; not for a cluster to an item, where 32 positions are
+// 5.9 us at 480 and 64 are 7.8), 16 of fp16 rows of 256.  The CTAs are those whose
 // registers need no spills to speak of: 12 warps of Q8_0 at 168 registers read the
 // ragged batch of 64 sequences in 39 us, 16 at 128 in 42.
 template <int T, int D, int NC, bool ONE>
 struct PagedCfg {
   static constexpr int ROW = kv_row_bytes<T>(D);
-  static constexpr int CH = ROW <= 72 && D * NC <= 128 ? 64 : ROW <= 272 ? 32 : 16;
+  static constexpr int CH = ROW <= 72 && D * NC <= 128 && !ONE ? 64 : ROW <= 272 ? 32 : 16;
   static constexpr int SLOTS = 3;
   static constexpr int FOURS = (D == 256 || (T == kKvF16 && D == 128)) ? 2 : D * NC <= 64 ? 4 : NC <= 2 ? 3 : 2;
   static constexpr int WARPS = ONE ? 8 : 4, CTAS = ONE ? FOURS / 2 : FOURS;
@@ -685,20 +686,24 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
 }
 
 // ONE: a cluster of 1 to 8 CTAs to an item, whose warps share its chunks out and join
-// through shared memory, the CTAs through the cluster's, in one launch.  Taken for at
-// most as many items as SMs, with as many CTAs as give each warp one chunk of the longest
-// sequence that the table can hold while they are at most three quarters of the SMs (all
-// clusters of 8 are then resident at once), and tables of at most kOneCtaCtx positions
-// for each of the CTAs; kOneCtaCtxMany where one CTA is all there is and the items are
-// half as many as the SMs.  Against parts and their join, Q8_0, 8 KV heads of 128, us on
-// the device:
-//   1 sequence of 145 / 480 / 1000 / 2049 / 4000 / 6000:
-//     4.2 / 6.2 / 6.9 / 7.9 / 8.4 / 10.2 against 7.0 / 8.0 / 8.3 / 8.8 / 9.7 / 10.4
-//   3 of 480 / 1000 / 2049: 6.3 / 7.0 / 10.1 against 8.4 / 8.9 / 10.6
-//   16 of 480 / 1000: 7.1 / 11.3 against 11.4 / 15.6
-//   64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
-// (not further for many: one long sequence among short ones would wait for its own warps).
-constexpr int kOneCtaCtx = 768, kOneCtaCtxMany = 1024;
+// through shared memory, the CTAs through the cluster's, in one launch.  Taken where all
+// clusters of as many CTAs as give each warp one chunk of the longest sequence that the
+// table can hold, or of 8, or as many as there is room for, are resident at once, and for
+// tables of at most kOneCtaCtx positions for each of the CTAs.  A group of more than four
+// query heads is cut into tiles of four where a warp's positions times heads are no more
+// for it: with more clusters, of shorter chains of instructions, which is what a warp
+// with one chunk takes its time for.  Against parts and their join, 8 KV heads of 128 in
+// Q8_0, us on the device:
+//   32 query heads, 1 sequence of 145 / 480 / 2049 / 4000 / 6000 / 8000:
+//     4.8 / 5.6 / 7.6 / 8.4 / 10.1 / 11.8 against 7.4 / 7.9 / 8.8 / 9.7 / 10.5 / 12.0
+//   64 query heads, 1 of 145 / 1000 / 2049 / 4000 / 6000:
+//     4.9 / 6.2 / 7.6 / 9.9 / 11.7 against 9.1 / 9.9 / 10.8 / 12.2 / 12.9 (tiles of eight:
+//     6.1 / 8.3 / 9.8 / 10.7 for the first four)
+//   3 of 1000 / 2049 / 4000: 6.3 / 8.1 / 11.1 against 9.1 / 10.8 / 13.1
+//   8 of 1000 / 2000: 8.2 / 11.8 against 11.4 / 14.0; 16 of 1000: 10.8 against 14.2
+//   1 of 15000: 17.9 against 13.8; 64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
+// (no further: one long sequence among short ones would wait for its own warps).
+constexpr int kOneCtaCtx = 1024;
 
 template <int T, int D, int NC, bool ONE>
 __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<T, D, NC, ONE>::CTAS)
@@ -1273,6 +1278,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
   cp_async_wait<0>();
 
   if constexpr (ONE) {
+    static_assert(F::WARPS == 8);
     auto at = [&](int w) { return reinterpret_cast<float*>(ring + w * F::PART); };
     __syncthreads();  // every warp is done with its ring
 #pragma unroll
@@ -1285,23 +1291,31 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
       store(ct, at(warp) + 2 * kMaxTile + h * D, 1.f);
     }
     __syncthreads();
-    // parts `at(0)` to `at(n - 1)` joined: elements 4 i to 4 i + 3 of the item's rows, and the row's (m, l)
+    // parts `at(0)` to `at(n - 1)`, 8 at most, joined: elements 4 i to 4 i + 3 of the item's rows, and the row's (m, l)
     auto join = [&](auto part_at, int n, int i, float2& ml) {
       const int h = i / (D / 4);
       float M = -INFINITY;
-#pragma unroll 8
-      for (int w = 0; w < n; ++w) M = fmaxf(M, part_at(w)[2 * h]);
+      float2 x[8];
+      float4 y[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        x[w] = make_float2(-INFINITY, 0.f);
+        y[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w < n) {
+          const float* p = part_at(w);
+          x[w] = *reinterpret_cast<const float2*>(p + 2 * h);
+          y[w] = reinterpret_cast<const float4*>(p + 2 * kMaxTile)[i];
+        }
+        M = fmaxf(M, x[w].x);
+      }
       const float base = M == -INFINITY ? 0.f : M;
       float L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int w = 0; w < n; ++w) {
-        const float* p = part_at(w);
-        const float2 x = *reinterpret_cast<const float2*>(p + 2 * h);
-        const float4 y = reinterpret_cast<const float4*>(p + 2 * kMaxTile)[i];
-        const float f = ex2(x.x - base);
-        L = fmaf(x.y, f, L);
-        O.x = fmaf(y.x, f, O.x); O.y = fmaf(y.y, f, O.y); O.z = fmaf(y.z, f, O.z); O.w = fmaf(y.w, f, O.w);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float f = ex2(x[w].x - base);
+        L = fmaf(x[w].y, f, L);
+        O.x = fmaf(y[w].x, f, O.x); O.y = fmaf(y[w].y, f, O.y); O.z = fmaf(y[w].z, f, O.z); O.w = fmaf(y[w].w, f, O.w);
       }
       ml = make_float2(M, L);
       return O;

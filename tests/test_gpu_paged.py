@@ -396,6 +396,22 @@ def test_attention_clusters(kind, d, hq, hkv, top):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 128), (18, 3, 64), (33, 3, 128), (32, 2, 256)])
+@pytest.mark.parametrize("top", [300, 700, 1090, 1500, 1800, 2049])
+def test_attention_clusters_of_any_size_and_tiles_of_four(kind, hq, hkv, d, top):
+    """Groups of 6 to 16 query heads, cut into tiles of four or not; clusters of 2 to 8 CTAs."""
+    check_attention(kind, hq, hkv, d, 16, [top], top + d)
+    check_attention(kind, hq, hkv, d, 16, [5, 0, top], top + d)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("top", [8192, 8193])
+def test_attention_both_sides_of_the_longest_cluster(kind, top):
+    check_attention(kind, 8, 1, 128, 16, [top], top)
+    check_attention(kind, 4, 1, 64, 16, [top], top)
+
+
+@pytest.mark.parametrize("kind", TYPES)
 def test_attention_one_cta_for_many_items(kind):
     """80 items (more than half of the SMs), tables of 1024 positions and of a page more."""
     lens = [1024, 1000, 0, 1, 33, 700, 513, 1023] + [5] * 32
