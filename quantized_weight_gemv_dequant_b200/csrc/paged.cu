@@ -172,7 +172,8 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int64_t grid
 
 // How a cluster of CTAs to an item runs: as many CTAs as give each warp one chunk of the
 // longest sequence that the table can hold, or the most of which all clusters are resident
-// at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each).
+// at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each; asked for once, the GPUs of
+// a machine being alike).
 struct OneGrid {
   int64_t items, work;  // work: a warp's positions times heads at most
   int most, ctas;       // 0: more items than CTAs are resident

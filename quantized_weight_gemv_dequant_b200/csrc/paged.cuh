@@ -700,9 +700,10 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
 //     4.9 / 6.2 / 7.6 / 9.9 / 11.7 against 9.1 / 9.9 / 10.8 / 12.2 / 12.9 (tiles of eight:
 //     6.1 / 8.3 / 9.8 / 10.7 for the first four)
 //   3 of 1000 / 2049 / 4000: 6.3 / 8.1 / 11.1 against 9.1 / 10.8 / 13.1
-//   8 of 1000 / 2000: 8.2 / 11.8 against 11.4 / 14.0; 16 of 1000: 10.8 against 14.2
+//   8 of 1000: 8.2 against 11.4; 16 of 480: 7.0 against 11.4
 //   1 of 15000: 17.9 against 13.8; 64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
-// (no further: one long sequence among short ones would wait for its own warps).
+//   3 of 1 to 4000: 10.8 against 9.5 (one long sequence among short ones waits for its own
+//   warps, so no further; F16 9.9 against 9.7, Q4_0 10.8 against 11.2)
 constexpr int kOneCtaCtx = 1024;
 
 template <int T, int D, int NC, bool ONE>
