@@ -346,7 +346,7 @@ NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_st
  *   on the GPU need workspaces of their own.
  * Limits: n_kv_heads | n_q_heads, at most 64 query heads per KV head; scale
  * finite; q and out 16-byte aligned, q_stride a multiple of 4; |scale q| below
- * 2^116 over block types.
+ * 2^127.
  * A length below 0 counts as 0 and one past max_pages * page_size as that; a
  * page outside the pool reads as keys and values of zero (status 5 for each).
  * Cache rows past a sequence's length are not used, whatever they hold. */

@@ -470,8 +470,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
 // scales times a power of two that puts the chunk's largest in [2^4, 2^5): nothing
 // overflows fp16, and what its subnormals round off is below 2^-35 of the largest
 // weight and 2^-29 of the chunk's largest value.
-// The matrix instruction's fp32 accumulation truncates, so it only sums one block
-// (keys) or one chunk (values); longer sums are ordinary fp32 adds.
+// Codes enter as signed integers: as (code + 128) or (code + 8), fp16 subnormals that
+// take no conversion, keys of Q4_0 would take 9 % less time (49.7 us for 131071
+// positions instead of 54.4) and of Q8_0 2 %, but a score would be off by a rounding of
+// the offset's share, 128 sum(q), whatever its own size: 20 times a plain fp32
+// evaluation's error where a block has one large key and queries have a mean.
+// The matrix instruction's fp32 accumulation truncates, so it only sums one block of
+// codes, one F16 key (head_dim / 16 instructions) or one chunk of values; longer sums
+// are ordinary fp32 adds.
 //
 // Work: the chunks of all items in a row, cut into equal parts, one per warp of
 // a grid that fills the GPU, whatever the lengths.  A part that holds a whole
@@ -895,18 +901,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
 
   // p is kept 2^kPBits fold, in l and o too
   constexpr float kPBits = T == kKvF16 ? 14.f : 10.f;
-  // Block types' keys enter the products as fp16 subnormals, (code + 128) 2^-24 or (code + 8) 2^-20: an instruction
-  // for two elements, no conversion.  The offset's share of a block's product is known with q and taken off in
-  // fp32.  (The instruction aligns its products by the operands' exponents, and a subnormal's is 2^-14: nibbles as
-  // 2^-24 would lie so far below that the output is off by 1e-6, instead of 4e-7.  Converted to normal numbers,
-  // 131071 positions of Q4_0 take 54 us instead of 49.  Not for values: all weights have one sign, and the
-  // offset's share would grow faster than the sum.)
-  constexpr float kCodeUnit = T == kKvQ8 ? 16777216.f : T == kKvQ4 ? 1048576.f : 1.f;
   // This lane's heads: t of column tile c as a softmax row (with positions g, g + 8 of 16)
   // and in o (with two elements of 16); g / 2 in q's fragments.
   uint32_t qf[NC][NB][4];
   float o[NC][NT][2], m[NC], l[NC], to_log2[NC];
-  float off[NC][NB];  // block types: minus the offset's share of a block's product
   bool fresh = true;
   int rows = min(F::HEADS, G - F::HEADS * cur.rt), head0 = cur.kvh * G + F::HEADS * cur.rt;
   if constexpr (ONE) {  // a warp without a chunk
@@ -963,10 +961,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
         const int es = eb == 255 ? 127 : min(254, 267 - eb);
         const float up = __int_as_float(es << 23);
         const float down = es == 254 ? __int_as_float(0x00400000) : __int_as_float((254 - es) << 23);
-        to_log2[ct] = __shfl_sync(0xffffffffu, scale * down * (1.44269504088896340736f * kCodeUnit), 8 * t);
+        to_log2[ct] = __shfl_sync(0xffffffffu, scale * down * 1.44269504088896340736f, 8 * t);
 #pragma unroll
         for (int i = 0; i < NB / 2; ++i) {
-          float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             // the pairs that a key fragment of this type has: elements 0 1, 2 3, ... or 0 2, 1 3, ... of this lane's
@@ -976,17 +973,6 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
             const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? hi : lo, 4);
             qf[ct][2 * i][j] = odd ? other : hi;
             qf[ct][2 * i + 1][j] = odd ? lo : other;
-            if constexpr (T != kKvF16) {
-              const float2 f = __half22float2(bits_h2(hi)), r = __half22float2(bits_h2(lo));
-              sum += (f.x + f.y) + (r.x + r.y);
-            }
-          }
-          if constexpr (T != kKvF16) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum *= -(T == kKvQ8 ? 128.f : 8.f) / kCodeUnit;
-            off[ct][2 * i] = __shfl_sync(0xffffffffu, sum, 8 * t);
-            off[ct][2 * i + 1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
           }
         }
 #pragma unroll
@@ -1041,16 +1027,15 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
             const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, 2 * b + (t >> 1)) * 16 + (t & 1) * 8;
             uint2 u = lds64(a), v = lds64(a + 8 * F::CB);
             u.x ^= 0x80808080u; u.y ^= 0x80808080u; v.x ^= 0x80808080u; v.y ^= 0x80808080u;
-            a0[0] = __byte_perm(u.x, 0, 0x4140); a0[1] = __byte_perm(v.x, 0, 0x4140);
-            a0[2] = __byte_perm(u.x, 0, 0x4342); a0[3] = __byte_perm(v.x, 0, 0x4342);
-            a1[0] = __byte_perm(u.y, 0, 0x4140); a1[1] = __byte_perm(v.y, 0, 0x4140);
-            a1[2] = __byte_perm(u.y, 0, 0x4342); a1[3] = __byte_perm(v.y, 0, 0x4342);
+            a0[0] = bytes_h2<0x4140>(u.x); a0[1] = bytes_h2<0x4140>(v.x);
+            a0[2] = bytes_h2<0x4342>(u.x); a0[3] = bytes_h2<0x4342>(v.x);
+            a1[0] = bytes_h2<0x4140>(u.y); a1[1] = bytes_h2<0x4140>(v.y);
+            a1[2] = bytes_h2<0x4342>(u.y); a1[3] = bytes_h2<0x4342>(v.y);
           } else {
             const uint32_t a = slot + (16 * k + g) * F::CB + swz_k<T, C>(g, b) * 16 + 4 * t;
-            constexpr uint32_t M = 0x00F000F0u;  // every nibble 16 fold
-            const uint32_t u = lds32(a), v = lds32(a + 8 * F::CB);
-            a0[0] = (u << 4) & M; a0[1] = (v << 4) & M; a0[2] = (u >> 4) & M; a0[3] = (v >> 4) & M;
-            a1[0] = u & M; a1[1] = v & M; a1[2] = (u >> 8) & M; a1[3] = (v >> 8) & M;
+            const uint32_t u = lds32(a), v = lds32(a + 8 * F::CB), u8 = u >> 8, v8 = v >> 8;
+            a0[0] = nib_lo(u); a0[1] = nib_lo(v); a0[2] = nib_lo(u8); a0[3] = nib_lo(v8);
+            a1[0] = nib_hi(u); a1[1] = nib_hi(v); a1[2] = nib_hi(u8); a1[3] = nib_hi(v8);
           }
           float d[2];
 #pragma unroll
@@ -1063,8 +1048,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
             float acc[4];
             mma16816_first(acc, a0, qf[ct][b][0], qf[ct][b][1]);
             mma16816(acc, a1, qf[ct][b][2], qf[ct][b][3]);
-            s[ct][k][0] = fmaf(acc[0] + acc[1] + off[ct][b], d[0], s[ct][k][0]);
-            s[ct][k][1] = fmaf(acc[2] + acc[3] + off[ct][b], d[1], s[ct][k][1]);
+            s[ct][k][0] = fmaf(acc[0] + acc[1], d[0], s[ct][k][0]);
+            s[ct][k][1] = fmaf(acc[2] + acc[3], d[1], s[ct][k][1]);
           }
         }
       }
