@@ -289,8 +289,9 @@ NTX_API uint64_t ntx_paged_kv_bytes(int type, int n_kv_heads, int head_dim, int 
  * Angles are formed in fp64 (off by up to 2^-51 of the angle), the rest in fp32.
  *   q, q_out: device fp32, token n's n_q_heads x head_dim values start at
  *   n * q_stride floats; k, k_out: n_kv_heads x head_dim at n * k_stride.
- *   q_out may be q and k_out may be k; any other overlap of an output with an
- *   input's rows is not allowed.  wq, wk: device fp32[head_dim].
+ *   q_out may be q and k_out may be k; any other overlap of an output's rows with
+ *   an input's, or with the other output's, is refused (NTX_ERR_INVALID_ARG; what
+ *   lies between rows may be anything's).  wq, wk: device fp32[head_dim].
  *   positions: device int32[n_tokens]; a negative one marks an unused row,
  *   whose outputs are left as they were.
  * head_dim even, 2..256; rot_dim even, 0..head_dim; strides at least the row
@@ -337,7 +338,7 @@ NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_st
  *   out[s][h] = sum_{p < ctx_lens[s]} softmax_p(scale q[s][h].k_p) v_p,
  * zeros where ctx_lens[s] is 0.  Scores, softmax statistics and sums are fp32.
  *   q: device fp32, sequence s's n_q_heads x head_dim values at s * q_stride
- *   floats.  out: device fp32 [n_seqs][n_q_heads][head_dim], not overlapping q.
+ *   floats.  out: device fp32 [n_seqs][n_q_heads][head_dim], not overlapping q's rows.
  *   ctx_lens: device int32[n_seqs]; counts the new token, whose key and value
  *   the caller has already appended.  The lengths may change between replays
  *   of a captured graph.

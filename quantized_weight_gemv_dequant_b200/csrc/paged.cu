@@ -26,13 +26,33 @@ int failf(int code, const char* fmt, ...) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
+// n rows of `width` floats, `stride` floats apart.
+struct Rows {
+  const float* first;
+  int64_t stride, width;
+};
+using wide_int = __int128;  // any stride that the arguments can hold
+wide_int floor_div(wide_int a, wide_int b) { return a / b - (a % b < 0); }  // b > 0
 
-// Bytes from the first to the last float of n rows.
-uint64_t span(int64_t n, int64_t stride, int64_t width) { return n < 1 ? 0 : ((n - 1) * stride + width) * 4ull; }
+// Whether a row of a and a row of b share a byte; what lies between rows does not count.
+bool rows_overlap(const Rows& a, const Rows& b, int64_t n) {
+  if (n < 1 || a.width < 1 || b.width < 1 || !a.first || !b.first) return false;
+  const wide_int x = reinterpret_cast<uintptr_t>(a.first), y = reinterpret_cast<uintptr_t>(b.first), d = y - x;
+  const wide_int sa = (wide_int)a.stride * 4, sb = (wide_int)b.stride * 4, wa = a.width * 4, wb = b.width * 4;
+  if (x + (n - 1) * sa + wa <= y || y + (n - 1) * sb + wb <= x) return false;  // apart as a whole, as most are
+  if (n == 1) return true;
+  // row i of a meets row j of b:  d - wa < i sa - j sb < d + wb
+  if (sa == sb) {
+    const wide_int lo = floor_div(d - wa, sa) + 1, hi = -floor_div(-(d + wb), sa) - 1;  // of i - j
+    return (lo > 1 - n ? lo : 1 - n) <= (hi < n - 1 ? hi : n - 1);
+  }
+  for (int64_t i = 0; i < n; ++i) {
+    const wide_int at = i * sa - d;  // at - wb < j sb < at + wa
+    const wide_int lo = floor_div(at - wb, sb) + 1, hi = -floor_div(-(at + wa), sb) - 1;
+    if ((lo > 0 ? lo : 0) <= (hi < n - 1 ? hi : n - 1)) return true;
+  }
+  return false;
+}
 
 int row_bytes(int type, int D) {
   switch (type) {
@@ -295,9 +315,10 @@ int ntx_qk_norm_rope(const float* q, const float* k, float* q_out, float* k_out,
   if (!aligned(q, 4) || !aligned(k, 4) || !aligned(q_out, 4) || !aligned(k_out, 4) || !aligned(wq, 4) ||
       !aligned(wk, 4) || !aligned(positions, 4))
     return failf(NTX_ERR_ALIGN, "%s: pointers must be 4-byte aligned", who);
-  const uint64_t bq = span(n_tokens, q_stride, nq), bk = span(n_tokens, k_stride, nk);
-  if ((nq && q != q_out && overlap(q, bq, q_out, bq)) || (nk && k != k_out && overlap(k, bk, k_out, bk)))
-    return failf(NTX_ERR_INVALID_ARG, "%s: an output partially overlaps its input", who);
+  const Rows rq{q, q_stride, nq}, rk{k, k_stride, nk}, rqo{q_out, q_stride, nq}, rko{k_out, k_stride, nk};
+  if ((q != q_out && rows_overlap(rq, rqo, n_tokens)) || (k != k_out && rows_overlap(rk, rko, n_tokens)) ||
+      rows_overlap(rq, rko, n_tokens) || rows_overlap(rk, rqo, n_tokens) || rows_overlap(rqo, rko, n_tokens))
+    return failf(NTX_ERR_INVALID_ARG, "%s: an output overlaps an input it does not replace, or the other output", who);
   const int heads = n_q_heads + n_kv_heads;
   // whole rows of 64, 128 or 256 in 16-byte pieces; the halves' pairs are as wide apart as the lanes only when all rotate
   const bool vec = (head_dim == 64 || head_dim == 128 || head_dim == 256) && rows16(q, q_stride) && rows16(k, k_stride) &&
@@ -393,7 +414,7 @@ int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stri
   if ((rc = check_kv_pointers(who, kv)) != NTX_OK) return rc;
   if (!aligned(q, 16) || !aligned(out, 16) || q_stride % 4 || !aligned(workspace, 16) || !aligned(ctx_lens, 4))
     return failf(NTX_ERR_ALIGN, "%s: q, its rows, out and workspace must be 16-byte aligned", who);
-  if (overlap(q, span(kv->n_seqs, q_stride, width), out, span(kv->n_seqs, width, width)))
+  if (rows_overlap({q, q_stride, width}, {out, width, width}, kv->n_seqs))
     return failf(NTX_ERR_INVALID_ARG, "%s: out overlaps q", who);
   if (ws_bytes < ntx_attn_paged_workspace_bytes(kv, n_q_heads))
     return failf(NTX_ERR_NOMEM, "%s: workspace too small", who);
