@@ -9,6 +9,7 @@
 #include "launch.h"
 #include "ntx.h"
 #include "paged.cuh"
+#include "per_device.h"
 
 namespace ntx {
 namespace {
@@ -192,8 +193,8 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int64_t grid
 
 // How a cluster of CTAs to an item runs: as many CTAs as give each warp one chunk of the
 // longest sequence that the table can hold, or the most of which all clusters are resident
-// at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each; asked for once, the GPUs of
-// a machine being alike).
+// at once (15 of 8 CTAs on a B200 of 148 SMs that hold one each; asked for once on a device,
+// so that the order of an output's sums does not depend on what ran on another).
 struct OneGrid {
   int64_t items, work;  // work: a warp's positions times heads at most
   int most, ctas;       // 0: more items than CTAs are resident
@@ -202,21 +203,22 @@ template <int T, int D, int NC>
 cudaError_t one_grid(const ntx_paged_kv& kv, int G, OneGrid* grid) {
   using O = PagedCfg<T, D, NC, true>;
   static std::atomic<unsigned long long> done{0};
-  static std::atomic<int> fit[9];  // 1 more than the clusters of that many CTAs that are resident at once
-  cudaError_t e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done);
-  if (e != cudaSuccess) return e;
+  static PerDevice<9> fit;  // clusters of that many CTAs that are resident at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (e = allow_smem(attn_paged_kernel<T, D, NC, true>, O::SMEM, done)) != cudaSuccess) return e;
   OneGrid g{(int64_t)kv.n_seqs * kv.n_kv_heads * ((G + O::HEADS - 1) / O::HEADS), 0, 0, 0};
   const int64_t chunks = ((int64_t)kv.max_pages * kv.page_size + O::CH - 1) / O::CH;
   for (int c = 1; c <= 8; ++c) {
-    int n = fit[c].load(std::memory_order_relaxed);
-    if (n == 0) {
+    int n;
+    e = fit.get(dev, c, &n, [&](int* clusters) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       one_config<O>(&cfg, attr, c, c, nullptr);
-      if ((e = cudaOccupancyMaxActiveClusters(&n, attn_paged_kernel<T, D, NC, true>, &cfg)) != cudaSuccess) return e;
-      fit[c].store(++n, std::memory_order_relaxed);
-    }
-    if (g.items >= n) continue;
+      return cudaOccupancyMaxActiveClusters(clusters, attn_paged_kernel<T, D, NC, true>, &cfg);
+    });
+    if (e != cudaSuccess) return e;
+    if (g.items > n) continue;
     g.most = c;
     if (g.ctas * O::WARPS < chunks) g.ctas = c;
   }
