@@ -350,7 +350,15 @@ NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_st
  * 2^127.
  * A length below 0 counts as 0 and one past max_pages * page_size as that; a
  * page outside the pool reads as keys and values of zero (status 5 for each).
- * Cache rows past a sequence's length are not used, whatever they hold. */
+ * Cache rows past a sequence's length are not used, whatever they hold.
+ * A NaN among a sequence's rows goes where the formula takes it.  Infinities do not
+ * (ntx_kv_append makes them of fp16 elements beyond 65504, and scales that are
+ * infinite of blocks beyond their largest): q and the weights enter the products as
+ * two numbers each, of which one can be zero or of the other sign.  An infinite value
+ * makes its column (block types: its block's) infinite or NaN, and over block types
+ * the other columns of its sequence and KV head inaccurate; with an infinite key the
+ * sequence's outputs over its KV head are NaN, or those without that position.
+ * Other sequences and heads are not touched. */
 NTX_API size_t ntx_attn_paged_workspace_bytes(const ntx_paged_kv* kv, int n_q_heads);
 NTX_API int ntx_attn_decode_paged(const ntx_paged_kv* kv, const float* q, int64_t q_stride, float* out, int n_q_heads,
                                   const int32_t* ctx_lens, float scale, void* workspace, size_t ws_bytes,
