@@ -45,6 +45,13 @@ enum : int {
   kChkGemvPartial = 10,  // per-op GEMV: row partials
   kChkAttnCtx = 11,      // per-op attention: the step's context inside the cache
   kChkKvAppendOp = 12,   // per-op Q/K/V epilogue: the KV cache position it appends
+  kChkPagedRow = 13,     // paged cache write and read: a row's codes and scales inside the pool
+  kChkPagedTable = 14,   // paged attention: the page table's entry
+  kChkPagedLoad = 15,    // paged attention: the rows it copies inside the pool
+  kChkPagedSlot = 16,    // paged attention: where a copy lands in its ring slot, the slot in the ring
+  kChkPagedPart = 17,    // paged attention: a part's record and rows
+  kChkPagedOut = 18,     // paged attention and its join: a row of the output
+  kChkPagedJoin = 19,    // paged attention's join: the parts it reads
 };
 #ifdef NTX_CHECK
 constexpr bool kCheck = true;

@@ -275,7 +275,7 @@ cudaError_t launch_attn_paged(const ntx_paged_kv& kv, const float* q, int64_t qs
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<D>, (const int4*)split, (const float*)part, out, Hq,
-                            G < F::HEADS ? G : F::HEADS);
+                            G < F::HEADS ? G : F::HEADS, kv.n_seqs, device_status_ptr());
 }
 
 int finish(const char* who, cudaError_t e) { return e == cudaSuccess ? NTX_OK : record_cuda_error(e, who); }

@@ -23,6 +23,12 @@ __host__ __device__ constexpr int kv_row_bytes(int D) {
   return kv_code_bytes<T>(D) + (T == kKvF16 ? 0 : D / 16);
 }
 
+// Bytes of a pool, for the debug build's checks.
+template <int T, int D>
+__device__ __forceinline__ int64_t kv_pool_bytes(const ntx_paged_kv& c) {
+  return (int64_t)c.n_pages * c.n_kv_heads * c.page_size * kv_row_bytes<T>(D);
+}
+
 __device__ __forceinline__ void bad_page(int* status) { atomicExch(status, (int)kStatusBadPage); }
 
 // Where (sequence, position) lies: the first byte of the page's part of head 0
@@ -75,6 +81,14 @@ struct PieceAt {
   }
   __device__ __forceinline__ uint16_t* scale(int i) const {
     return reinterpret_cast<uint16_t*>(scales + i * 128 / D * head_bytes + i * 128 % D / 16);
+  }
+  // (debug build) whether this lane's codes and scale of step i lie in the pool
+  __device__ __forceinline__ bool inside(const ntx_paged_kv& c, const void* pool, int i, int* status) const {
+    const uint8_t* base = static_cast<const uint8_t*>(pool);
+    const int64_t bytes = kv_pool_bytes<T, D>(c);
+    return chk(status, kChkPagedRow, code(i) - base, bytes) &&
+           chk(status, kChkPagedRow, code(i) - base + (T == kKvF16 ? 7 : 3), bytes) &&
+           (T == kKvF16 || chk(status, kChkPagedRow, reinterpret_cast<const uint8_t*>(scale(i)) - base + 1, bytes));
   }
 };
 
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_append_kernel(const ntx_p
   for (int i = 0; i < kPieceSteps; ++i) {
     const int e = e0 + i * 128;
     if (e - lane * 4 >= width) break;
-    const bool on = e < width;
+    const bool on = e < width && at.inside(c, is_v ? c.v_pages : c.k_pages, i, status);
     if constexpr (T == kKvF16) {
       if (on) {
         uint2 h;
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_pag
 #pragma unroll
   for (int i = 0; i < kPieceSteps; ++i) {
     const int e = e0 + i * 128;
-    if (e >= width) break;
+    if (e >= width || !at.inside(c, is_v ? c.v_pages : c.k_pages, i, status)) break;
     if constexpr (T == kKvF16) {
       code[i] = *reinterpret_cast<const uint2*>(at.code(i));
     } else {
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv_read_kernel(const ntx_pag
 #pragma unroll
   for (int i = 0; i < kPieceSteps; ++i) {
     const int e = e0 + i * 128;
-    if (e >= width) break;
+    if (e >= width || !at.inside(c, is_v ? c.v_pages : c.k_pages, i, status)) break;
     float4 o;
     if constexpr (T == kKvF16) {
       o = make_float4(half_bits_to_float(code[i].x), half_bits_to_float(code[i].x >> 16),
@@ -807,7 +821,10 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
       ld_first[r] = ld_row;
-      ld_page[r] = ld.ci * CH + 16 * r < ld.len ? __ldg(row + ld_j) : -1;
+      ld_page[r] = ld.ci * CH + 16 * r < ld.len &&
+                           chk(status, kChkPagedTable, (int64_t)ld.s * c.max_pages + ld_j, (int64_t)c.n_seqs * c.max_pages)
+                       ? __ldg(row + ld_j)
+                       : -1;
       if ((ld_row += 16) == c.page_size) {
         ld_row = 0;
         ++ld_j;
@@ -834,6 +851,12 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
             if (lane == 0) bad_page(status);
             rows = 0;
           }
+          if constexpr (kCheck) {  // (debug build) the rows' last code and scale, and their slot
+            const int64_t part = ((int64_t)page * c.n_kv_heads + ld.kvh) * head_bytes, end = ld_first[r] + min(rows, 16);
+            if (rows > 0 && !(chk(status, kChkPagedLoad, part + end * F::CB - 1, kv_pool_bytes<T, D>(c)) &&
+                              chk(status, kChkPagedLoad, part + scales_at + end * F::SB - 1, kv_pool_bytes<T, D>(c))))
+              rows = 0;
+          }
           if (rows <= 0) page = 0;
           ld_rows[r] = rows;
           ld_at[r] = ((int64_t)page * c.n_kv_heads + ld.kvh) * head_bytes + lane_off;
@@ -846,17 +869,24 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
           constexpr int RPI = C >= 32 ? 1 : 32 / C;  // rows per i
           return (dst ^ ((V ? swz8<C>(i * RPI, 0) : swz_k<T, C>(i * RPI, 0)) * 16)) + i * RPI * F::CB;
         };
+        // (debug build) a piece's place inside its slot's codes, or scales, and the slot inside the ring
+        auto in_slot = [&](uint32_t to, int first, int end) {
+          return chk(status, kChkPagedSlot, (int64_t)to - ld_slot - first, end - first - 15) &&
+                 chk(status, kChkPagedSlot, (int64_t)ld_slot - smem_addr(ring) + F::SLOT - 1, F::RING);
+        };
+        constexpr int kCodes = CH * F::CB;
         if (ld_rows[r] >= 16) {
 #pragma unroll
-          for (int i = 0; i < C / 2; ++i) cp_async16(place(i), codes + i * 512);
-          if (F::SB > 0 && lane < F::SB) cp_async16(dst_sc, sc);
+          for (int i = 0; i < C / 2; ++i)
+            if (in_slot(place(i), 0, kCodes)) cp_async16(place(i), codes + i * 512);
+          if (F::SB > 0 && lane < F::SB && in_slot(dst_sc, kCodes, F::SLOT)) cp_async16(dst_sc, sc);
         } else {
 #pragma unroll
           for (int i = 0; i < C / 2; ++i) {
             const bool on = i * (32 / C) + lane / C < ld_rows[r];
-            cp_async16_fill(place(i), on ? codes + i * 512 : pool, on ? 16 : 0);
+            if (in_slot(place(i), 0, kCodes)) cp_async16_fill(place(i), on ? codes + i * 512 : pool, on ? 16 : 0);
           }
-          if (F::SB > 0 && lane < F::SB) {
+          if (F::SB > 0 && lane < F::SB && in_slot(dst_sc, kCodes, F::SLOT)) {
             const int valid = max(0, min(16, ld_rows[r] * F::SB - lane * 16));
             cp_async16_fill(dst_sc, valid ? sc : pool, valid);
           }
@@ -916,6 +946,9 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
       for (int n = 0; n < NT; ++n) o[ct][n][0] = o[ct][n][1] = 0.f;
     }
   }
+  auto in_out = [&](int s, int head) {  // (debug build) a row of the output
+    return chk(status, kChkPagedOut, s, c.n_seqs) && chk(status, kChkPagedOut, head, Hq);
+  };
   // this lane's elements of o, times f, to a row
   auto store = [&](int ct, float* dst, float f) {
 #pragma unroll
@@ -1234,7 +1267,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
         // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
         const int64_t at = 2ll * wid + (item_head ? 1 : 0);
         float* p = part + at * paged_part_floats(min(F::HEADS, G), D);
-        if (!whole && lane == 0) {  // the item's first warp and number of parts, where its output goes
+        if (!whole && lane == 0 && chk(status, kChkPagedPart, at, 2ll * all_warps)) {  // the item's first warp and number of parts, where its output goes
           const PagedParts parts = s_parts[warp];
           // units up to the chunk after this one, less the item's own
           const int64_t first = parts.begin(wid + 1) - max((int64_t)0, todo + (item_end ? kItemUnits : 0)) - cur.ci - 1;
@@ -1248,8 +1281,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
           for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
           if (h >= rows) continue;
           if (whole) {
-            store(ct, out + ((int64_t)cur.s * Hq + head0 + h) * D, 1.f / l[ct]);
-          } else {
+            if (in_out(cur.s, head0 + h)) store(ct, out + ((int64_t)cur.s * Hq + head0 + h) * D, 1.f / l[ct]);
+          } else if (chk(status, kChkPagedPart, at, 2ll * all_warps) && chk(status, kChkPagedPart, h, min(F::HEADS, G))) {
             if (g == 0) *reinterpret_cast<float2*>(p + 2 * h) = make_float2(m[ct], l[ct]);
             store(ct, p + 2 * kMaxTile + h * D, 1.f);
           }
@@ -1266,13 +1299,16 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
   if constexpr (ONE) {
     static_assert(F::WARPS == 8);
     auto at = [&](int w) { return reinterpret_cast<float*>(ring + w * F::PART); };
+    auto in_part = [&](int w, int h) {  // (debug build) a row of a part
+      return chk(status, kChkPagedPart, (w + 1ll) * F::PART - 1, F::SMEM) && chk(status, kChkPagedPart, h, F::HEADS);
+    };
     __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int ct = 0; ct < NC; ++ct) {
       const int h = 4 * ct + t;
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[ct] += __shfl_xor_sync(0xffffffffu, l[ct], x);
-      if (h >= rows) continue;
+      if (h >= rows || !in_part(warp, h)) continue;
       if (g == 0) *reinterpret_cast<float2*>(at(warp) + 2 * h) = make_float2(m[ct], l[ct]);
       store(ct, at(warp) + 2 * kMaxTile + h * D, 1.f);
     }
@@ -1307,6 +1343,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
       return O;
     };
     auto finish = [&](int i, float4 O, float L) {
+      if (!in_out(item_s, head0 + i / (D / 4))) return;
       const float f = empty ? 0.f : 1.f / L;  // an empty sequence: zeros
       reinterpret_cast<float4*>(out + ((int64_t)item_s * Hq + head0) * D)[i] =
           make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
@@ -1325,6 +1362,7 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
       float* own = at(F::WARPS);
       for (int i = threadIdx.x; i < pieces; i += F::WARPS * 32) {
         const float4 O = join(at, F::WARPS, i, ml);
+        if (!in_part(F::WARPS, i / (D / 4))) continue;
         reinterpret_cast<float4*>(own + 2 * kMaxTile)[i] = O;
         if (i % (D / 4) == 0) *reinterpret_cast<float2*>(own + 2 * (i / (D / 4))) = ml;
       }
@@ -1403,7 +1441,8 @@ struct PagedMerge {  // a running join of parts, four elements a thread
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int4* split, const float* part,
-                                                                      float* __restrict__ out, int Hq, int rows_max) {
+                                                                      float* __restrict__ out, int Hq, int rows_max,
+                                                                      int n_seqs, int* status) {
   __shared__ float s_m[kJoinWarps][4], s_l[kJoinWarps][4];
   __shared__ __align__(16) float4 s_o[kJoinWarps][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = blockIdx.x;
@@ -1415,6 +1454,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_paged_join_kernel(const int
     const int4 it = both[k];  // first warp, parts, sequence, first head and number of heads
     if (it.y == 0) continue;
     const int heads = it.w & 31;
+    if constexpr (kCheck) {  // (debug build) the item's parts, their rows, its output
+      if (!(chk(status, kChkPagedJoin, it.x, w + 1ll) && chk(status, kChkPagedJoin, it.x + it.y - 1ll, gridDim.x) &&
+            chk(status, kChkPagedJoin, heads - 1, rows_max) && chk(status, kChkPagedOut, it.z, n_seqs) &&
+            chk(status, kChkPagedOut, (it.w >> 5) + heads - 1, Hq)))
+        continue;
+    }
     const float* base = part + 2ll * it.x * stride;  // the first part is in slot 1 of its warp, the others in slot 0
     auto at = [&](int i) { return base + (2ll * i + (i == 0)) * stride; };
     float* to = out + ((int64_t)it.z * Hq + (it.w >> 5)) * D;
