@@ -290,7 +290,9 @@ NTX_API uint64_t ntx_paged_kv_bytes(int type, int n_kv_heads, int head_dim, int 
  *   theta^(-2i/rot_dim), i < rot_dim/2, with (a, b) = elements (2i, 2i+1)
  *   (NTX_ROPE_ADJACENT, the pairing of ntx_rope) or (i, i + rot_dim/2)
  *   (NTX_ROPE_HALVES); elements from rot_dim on are only normed.
- * Angles are formed in fp64 (off by up to 2^-51 of the angle), the rest in fp32.
+ * Angles are formed in fp64 (off by up to 2^-51 of the angle) and reduced there to at
+ * most an eighth of a turn, which is rounded to fp32 (2e-8); sine, cosine and the
+ * rest are fp32, so a head's sum of squares has to stay in fp32's range.
  *   q, q_out: device fp32, token n's n_q_heads x head_dim values start at
  *   n * q_stride floats; k, k_out: n_kv_heads x head_dim at n * k_stride.
  *   q_out may be q and k_out may be k; any other overlap of an output's rows with
@@ -340,7 +342,14 @@ NTX_API int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_st
 /* Attention of one new token per sequence over the paged cache: for sequence s
  * and query head h (KV head h / (n_q_heads/n_kv_heads)),
  *   out[s][h] = sum_{p < ctx_lens[s]} softmax_p(scale q[s][h].k_p) v_p,
- * zeros where ctx_lens[s] is 0.  Scores, softmax statistics and sums are fp32.
+ * zeros where ctx_lens[s] is 0.  Scores, softmax statistics and sums are fp32.  Keys
+ * and values enter the products exactly; an element of q and a weight as the sum of
+ * two fp16 numbers, off by at most 2^-22 of itself or, where that is more, 2^-38 of
+ * the head's largest q, 2^-35 of the largest weight (2^-30 where the value scales of
+ * 64 positions are all below 2^-14); a value block's scale by at most 2^-29 of the
+ * largest among 64 positions of its KV head.  The error against 64 bits is of the
+ * size of a plain fp32 evaluation's, and at most twice that where keys have channels
+ * far larger than the rest and queries a mean.
  *   q: device fp32, sequence s's n_q_heads x head_dim values at s * q_stride
  *   floats.  out: device fp32 [n_seqs][n_q_heads][head_dim], not overlapping q's rows.
  *   ctx_lens: device int32[n_seqs]; counts the new token, whose key and value

@@ -373,9 +373,10 @@ int ntx_kv_append(const ntx_paged_kv* kv, const float* k, const float* v, int64_
   const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
     return with_dim(kv->head_dim, [&](auto d) {
-    kv_append_kernel<decltype(t)::value, decltype(d)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
-        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
-    return cudaGetLastError();
+      kv_append_kernel<decltype(t)::value, decltype(d)::value>
+          <<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+              *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
+      return cudaGetLastError();
     });
   }));
 }
@@ -389,9 +390,10 @@ int ntx_kv_read(const ntx_paged_kv* kv, float* k, float* v, int64_t k_stride, in
   const int pieces = token_pieces(kv);
   return finish(who, with_type(kv->type, [&](auto t) {
     return with_dim(kv->head_dim, [&](auto d) {
-    kv_read_kernel<decltype(t)::value, decltype(d)::value><<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
-        *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
-    return cudaGetLastError();
+      kv_read_kernel<decltype(t)::value, decltype(d)::value>
+          <<<token_grid(n_tokens, 2 * pieces), kTokenWarps * 32, 0, (cudaStream_t)stream>>>(
+              *kv, k, v, k_stride, v_stride, seq_ids, positions, n_tokens, vec, pieces, device_status_ptr());
+      return cudaGetLastError();
     });
   }));
 }

@@ -56,9 +56,10 @@ __device__ __forceinline__ bool kv_place(const ntx_paged_kv& c, int seq, int pos
 // tokens of 8 heads of 128 from Q8_0: 43 us, 5.7 TB/s, 0.87 of a copy's bandwidth;
 // 16384 tokens to Q4_0 and back: 65 us (with a search of the first largest by ballot
 // and separate checks of zeros and infinities in every block: 69), 28 of them the read
-// at 5.4 TB/s.  The write to 4 bits is bound by its instructions, everything else by
-// memory.  Pieces of 1024 elements are 3 % faster on long prompts and 25 % slower on one
-// token.
+// at 5.6 TB/s.  Writes alone, 16384 tokens: F16 31 us (0.99 of a copy's bandwidth),
+// Q8_0 36 (0.72), Q4_0 38 (0.61): block types are bound by their instructions, the F16
+// write and the reads by memory.  Pieces of 1024 elements are 3 % faster on long prompts
+// and 25 % slower on one token.
 constexpr int kPieceSteps = 4, kPiece = kPieceSteps * 128;
 constexpr int kTokenWarps = 4;  // tokens of a CTA
 
@@ -313,7 +314,9 @@ __device__ __forceinline__ float2 rope_turn(double t) {
 // copy's bandwidth (angles shared by a CTA through shared memory: 117 us; sines and
 // cosines in fp64: 110; a tile's next rows loaded ahead: 138, the registers cost a
 // CTA).  VEC: rows are 16-byte aligned and a lane holds P consecutive pairs;
-// otherwise pairs lane, lane + 32, ...
+// otherwise pairs lane, lane + 32, ... with 4-byte accesses: over one buffer again and
+// again, half of each head rotated in halves takes 121 us, rows off by 4 bytes 126,
+// where aligned rows take 110.
 constexpr int kRopeWarps = 8;
 __host__ __device__ constexpr int rope_ctas(int P) { return P < 4 ? 4 : 3; }  // per SM, 64 and 80 registers
 template <int P, bool HALVES, bool VEC>
@@ -501,14 +504,14 @@ __global__ void __launch_bounds__(kRopeWarps * 32, rope_ctas(P))
 // barrier.  The order of every sum is fixed by lengths and grid.
 //
 // Why not the fifth-generation tensor cores: the work is bound by memory (F16) or by
-// taking codes apart (block types), not by products (hmma pipe at 0.10 to 0.16), and
+// taking codes apart (block types), not by products (hmma pipe at 0.10 to 0.17), and
 // their operands would have to pass through shared memory once more.
 //
 // Measured on B200, 32 query heads over 8 KV heads of 128, with the join: one fp16
 // sequence of 131071 positions 88 us (6.1 TB/s, 0.93 of a copy's bandwidth; without
-// the join 84); Q8_0 53 us (0.82), Q4_0 49 us (0.47: 870 instructions a chunk of 32
-// positions, issue at 0.63); 64 sequences of 1 to 8191 positions in Q8_0 38.5 us
-// (0.72).  Before items' starts counted as work the longest-running SM of that batch
+// the join 84); Q8_0 54 us (0.81), Q4_0 54.5 us (0.42: 940 instructions a chunk of 32
+// positions, issue at 0.61); 64 sequences of 1 to 8191 positions in Q8_0 39 us
+// (0.71).  Before items' starts counted as work the longest-running SM of that batch
 // took 80 k cycles where the others took 64 k.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -602,11 +605,12 @@ constexpr int kMaxTile = 16;  // heads of a tile at most: a part is (m, l)[16], 
 __host__ __device__ constexpr int paged_part_floats(int rows, int D) { return rows * D + 2 * kMaxTile; }
 
 // Positions per chunk, ring slots (one K or V chunk each) and CTAs per SM.  A chunk is
-// 2 to 8 KiB of keys: 64 positions of the narrow rows (4-bit rows of 128: 131071
-// positions in 49 us, 52 with 32; not for a cluster to an item, where 32 positions are
-// 5.9 us at 480 and 64 are 7.8), 16 of fp16 rows of 256.  The CTAs are those whose
-// registers need no spills to speak of: 12 warps of Q8_0 at 168 registers read the
-// ragged batch of 64 sequences in 39 us, 16 at 128 in 42.
+// 2 to 8 KiB of keys: 64 positions of the narrow rows (131071 positions of 4 KV
+// heads of 64 in Q8_0 in 26.4 us, 28.1 with 32; of 8 of 128 in 4 bits 53.7 and 54.6; not
+// for a cluster to an item, where 32 positions are 5.6 us at 480 and 64 are 7.2), 16 of
+// fp16 rows of 256.  The CTAs are those whose registers need no spills to speak of: 12
+// warps of Q8_0 at 168 registers read the ragged batch of 64 sequences in 39 us, 16 at
+// 128 in 41, and 131071 positions in 57 where 16 take 65.
 template <int T, int D, int NC, bool ONE>
 struct PagedCfg {
   static constexpr int ROW = kv_row_bytes<T>(D);
@@ -715,15 +719,16 @@ __device__ __forceinline__ int64_t lane_units(const ntx_paged_kv& c, const int* 
 // with one chunk takes its time for.  Against parts and their join, 8 KV heads of 128 in
 // Q8_0, us on the device:
 //   32 query heads, 1 sequence of 145 / 480 / 2049 / 4000 / 6000 / 8000:
-//     4.8 / 5.6 / 7.6 / 8.4 / 10.1 / 11.8 against 7.4 / 7.9 / 8.8 / 9.7 / 10.5 / 12.0
+//     4.6 / 5.6 / 7.6 / 8.3 / 10.1 / 11.8 against 7.5 / 8.2 / 9.0 / 9.9 / 10.6 / 12.0
 //   64 query heads, 1 of 145 / 1000 / 2049 / 4000 / 6000:
-//     4.9 / 6.2 / 7.6 / 9.9 / 11.7 against 9.1 / 9.9 / 10.8 / 12.2 / 12.9 (tiles of eight:
-//     6.1 / 8.3 / 9.8 / 10.7 for the first four)
-//   3 of 1000 / 2049 / 4000: 6.3 / 8.1 / 11.1 against 9.1 / 10.8 / 13.1
-//   8 of 1000: 8.2 against 11.4; 16 of 480: 7.0 against 11.4
-//   1 of 15000: 17.9 against 13.8; 64 of 1 to 400: 16.9 against 11.1 (more items than SMs)
-//   3 of 1 to 4000: 10.8 against 9.5 (one long sequence among short ones waits for its own
-//   warps, so no further; F16 9.9 against 9.7, Q4_0 10.8 against 11.2)
+//     4.8 / 6.2 / 7.7 / 10.1 / 12.0 against 8.8 / 9.7 / 10.6 / 12.0 / 13.2 (tiles of eight:
+//     6.2 / 7.8 / 9.7 / 10.5 / 12.8)
+//   3 of 1000 / 2049 / 4000: 6.2 / 8.1 / 11.3 against 9.1 / 10.8 / 13.1
+//   8 of 1000: 8.3 against 11.6; 16 of 480: 7.0 against 11.5
+//   1 of 15000: 18.1 against 13.9; 64 of 1 to 400: 19.5 against 13.5 (more items than SMs)
+//   one long sequence among short ones waits for its own warps: 7, 91 and 4000: 11.3
+//   against 9.7, 3, 4000 and 564: 11.1 against 9.5 (F16 9.9 against 9.6, Q4_0 11.1 against
+//   11.3), 4000, 2595 and 2: 11.0 against 10.6
 constexpr int kOneCtaCtx = 1024;
 
 template <int T, int D, int NC, bool ONE>
@@ -1267,7 +1272,8 @@ __global__ void __launch_bounds__(PagedCfg<T, D, NC, ONE>::WARPS * 32, PagedCfg<
         // slot 1: an item that this part begins, for others to end; slot 0: one that another part began
         const int64_t at = 2ll * wid + (item_head ? 1 : 0);
         float* p = part + at * paged_part_floats(min(F::HEADS, G), D);
-        if (!whole && lane == 0 && chk(status, kChkPagedPart, at, 2ll * all_warps)) {  // the item's first warp and number of parts, where its output goes
+        // the item's first warp and number of parts, where its output goes
+        if (!whole && lane == 0 && chk(status, kChkPagedPart, at, 2ll * all_warps)) {
           const PagedParts parts = s_parts[warp];
           // units up to the chunk after this one, less the item's own
           const int64_t first = parts.begin(wid + 1) - max((int64_t)0, todo + (item_end ? kItemUnits : 0)) - cur.ci - 1;
